@@ -11,6 +11,7 @@ outputs and return them.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -23,7 +24,7 @@ LIB_PATH = os.path.join(_PKG, "libfp4.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fp4.h")
 
 # fp4_status / fp4_dtype / fp4_format values (include/fp4.h).
-OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_ALIGN, ERR_NONFINITE, ERR_RANGE, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT = range(9)
+OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_ALIGN, ERR_NONFINITE, ERR_RANGE, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_INDEX = range(10)
 F32, BF16 = 0, 1
 NVFP4, MXFP4 = 0, 1
 MX_FLOOR, MX_CEIL = 0, 1
@@ -88,6 +89,12 @@ def lib() -> ctypes.CDLL:
             "fp4_nvfp4_quantize_columns": (I, [P, I, I64, I64, P, P, P, P, SZ, P, P]),
             "fp4_nvfp4_quantize_columns_with_amax": (I, [P, I, I64, I64, P, P, P, P, P, P]),
             "fp4_mxfp4_quantize_columns": (I, [P, I, I64, I64, I, P, P, P, P]),
+            "fp4_kv_write": (I, [P, P, P, I, I64, I64, I64, P, I, P, P]),
+            "fp4_kv_read": (I, [P, P, I64, P, P, I, I64, I64, P, P]),
+            "fp4_kv_attention_workspace_bytes": (SZ, [P, I64, I64, I64, I64]),
+            "fp4_kv_attention": (I, [P, P, I, I64, I64, I64, I64, P, I64, P, ctypes.c_float, I64, P, P, P, SZ, P, P]),
+            "fp4_linear_workspace_bytes": (SZ, [I64, I64]),
+            "fp4_linear": (I, [I, P, I, I64, I64, I64, P, P, P, I64, P, I, P, SZ, P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -546,6 +553,264 @@ def dequantize_grouped(qs, out_dtype=torch.bfloat16, outs=None, stream=None) -> 
     _check(fp4_dequantize_grouped(fmts.pop() if fmts else NVFP4, dequant_items(qs, ys), code, stream),
            "fp4_dequantize_grouped")
     return ys
+
+
+# ------------------------------------------- single-token serving -----------
+
+def _cuda(t: torch.Tensor, what: str, dtype=None):
+    if not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA tensor required")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: {dtype} required, got {t.dtype}")
+    return t
+
+
+def _on(device: torch.device):
+    """Makes `device` the current one for a call; the library launches on the current device."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors of a call live on one device: {device} and {t.device}")
+
+
+class KVCacheStruct(ctypes.Structure):
+    """struct fp4_kv_cache (include/fp4.h)."""
+    _fields_ = [("format", ctypes.c_int), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+                ("k_packed", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_packed", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_global_scale", ctypes.c_void_p),
+                ("v_global_scale", ctypes.c_void_p)]
+
+
+class KVCache:
+    """A paged FP4 cache of keys and values over the caller's tensors:
+    packed codes [pages, heads, page_size, head_dim/2] and scale bytes
+    [pages, heads, page_size, head_dim/G] (uint8, contiguous) of each, and
+    for NVFP4 one fp32 global scale per head.  `status` is the device word
+    that its calls report data errors in (`check()` reads it)."""
+
+    def __init__(self, fmt, k_packed, k_scales, v_packed, v_scales, k_global_scale=None, v_global_scale=None,
+                 status=None):
+        if fmt not in (NVFP4, MXFP4):
+            raise ValueError("fmt: NVFP4 or MXFP4")
+        group = 16 if fmt == NVFP4 else 32
+        dev = _cuda(k_packed, "k_packed").device
+        _same_device(dev, k_scales, v_packed, v_scales, status)
+        for name, t in (("k_packed", k_packed), ("k_scales", k_scales), ("v_packed", v_packed), ("v_scales", v_scales)):
+            if t.dtype != torch.uint8 or t.dim() != 4 or not t.is_contiguous():
+                raise ValueError(f"{name}: contiguous uint8 [pages, heads, page_size, bytes] required")
+        self.num_pages, self.heads, self.page_size, half = k_packed.shape
+        self.head_dim = half * 2
+        scales = (self.num_pages, self.heads, self.page_size, self.head_dim // group)
+        if v_packed.shape != k_packed.shape or k_scales.shape != scales or v_scales.shape != scales:
+            raise ValueError("keys and values share one shape, with one scale byte for each block of head_dim")
+        if fmt == NVFP4:
+            for name, g in (("k_global_scale", k_global_scale), ("v_global_scale", v_global_scale)):
+                if g is None or g.dtype != torch.float32 or g.shape != (self.heads,) or not g.is_contiguous():
+                    raise ValueError(f"{name}: contiguous float32 [heads] required for NVFP4")
+            _same_device(dev, k_global_scale, v_global_scale)
+        self.fmt, self.device = fmt, dev
+        self.k_packed, self.k_scales, self.v_packed, self.v_scales = k_packed, k_scales, v_packed, v_scales
+        self.k_global_scale, self.v_global_scale = k_global_scale, v_global_scale
+        self.status = status if status is not None else new_status(dev)
+        nv = fmt == NVFP4
+        self._struct = KVCacheStruct(fmt, self.heads, self.head_dim, self.page_size, self.num_pages, _p(k_packed),
+                                     _p(k_scales), _p(v_packed), _p(v_scales), _p(k_global_scale) if nv else None,
+                                     _p(v_global_scale) if nv else None)
+        self._ref = ctypes.addressof(self._struct)
+
+    def check(self, where: str = "KVCache"):
+        st = int(self.status.item())
+        if st != OK:
+            raise FP4Error(st, where)
+        return self
+
+
+def kv_cache(num_pages: int, heads: int, head_dim: int, page_size: int = 64, fmt: int = NVFP4, k_global_scale=None,
+             v_global_scale=None, device="cuda") -> KVCache:
+    """An empty (zero-filled) cache.  NVFP4 global scales: one number or a
+    [heads] tensor each, amax / 2688 of a calibration run (default 1 / 64:
+    values up to 42 before they saturate)."""
+    group = 16 if fmt == NVFP4 else 32
+
+    def zeros(last):
+        return torch.zeros((num_pages, heads, page_size, last), dtype=torch.uint8, device=device)
+
+    def scale(g):
+        if fmt != NVFP4:
+            return None
+        g = torch.as_tensor(1 / 64 if g is None else g, dtype=torch.float32, device=device)
+        return g.expand(heads).contiguous()
+    return KVCache(fmt, zeros(head_dim // 2), zeros(head_dim // group), zeros(head_dim // 2),
+                   zeros(head_dim // group), scale(k_global_scale), scale(v_global_scale))
+
+
+def _token_rows(t: torch.Tensor, what: str, tokens: int, heads: int, dim: int) -> int:
+    """Token stride of a [tokens, heads, dim] tensor whose heads and elements are contiguous."""
+    if t.shape != (tokens, heads, dim):
+        raise ValueError(f"{what}: [{tokens}, {heads}, {dim}] required, got {list(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{what}: contiguous heads and elements required")
+    return t.stride(0) if tokens > 1 else heads * dim
+
+
+def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rule: int = MX_FLOOR, status=None,
+             stream=None) -> None:
+    """Quantise k, v [tokens, heads, head_dim] (bf16 or fp32; views of a fused
+    projection may keep their token stride) into the cache's `slots` (int64
+    [tokens], negative = padding).  Data errors go to `status` (default: the
+    cache's)."""
+    T = slots.numel()
+    _cuda(slots, "slots", torch.int64)
+    if k.dtype != v.dtype or not slots.is_contiguous():
+        raise ValueError("k and v share one dtype; slots contiguous")
+    ks, vs = (_token_rows(t, n, T, cache.heads, cache.head_dim) for t, n in ((k, "k"), (v, "v")))
+    st = status if status is not None else cache.status
+    _same_device(cache.device, k, v, slots, st)
+    with _on(cache.device):
+        _check(lib().fp4_kv_write(cache._ref, _p(k), _p(v), _dtype_code(k), T, ks, vs, _p(slots), rule, _p(st),
+                                  _stream(stream)), "fp4_kv_write")
+
+
+def kv_read(cache: KVCache, slots: torch.Tensor, out_dtype=torch.bfloat16, k=None, v=None, status=None, stream=None):
+    """The keys and values in `slots` (int64 [tokens]; negative gives zeros)
+    as [tokens, heads, head_dim] tensors of out_dtype, or into k and v."""
+    T = slots.numel()
+    _cuda(slots, "slots", torch.int64)
+    shape = (T, cache.heads, cache.head_dim)
+    k = torch.empty(shape, dtype=out_dtype, device=cache.device) if k is None else k
+    v = torch.empty(shape, dtype=k.dtype, device=cache.device) if v is None else v
+    if k.dtype != v.dtype or not slots.is_contiguous():
+        raise ValueError("k and v share one dtype; slots contiguous")
+    ks, vs = (_token_rows(t, n, *shape) for t, n in ((k, "k"), (v, "v")))
+    st = status if status is not None else cache.status
+    _same_device(cache.device, k, v, slots, st)
+    with _on(cache.device):
+        _check(lib().fp4_kv_read(cache._ref, _p(slots), T, _p(k), _p(v), _dtype_code(k), ks, vs, _p(st),
+                                 _stream(stream)), "fp4_kv_read")
+    return k, v
+
+
+def kv_attention_workspace(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor) -> torch.Tensor:
+    """A zero-filled workspace for kv_attention calls of these shapes (or
+    smaller batches of them) on one stream at a time."""
+    B, L, HQ, _ = q.shape
+    n = lib().fp4_kv_attention_workspace_bytes(cache._ref, B, L, HQ, page_table.shape[1])
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=cache.device)
+
+
+def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, scale=None,
+                 window: int = 0, out=None, lse=None, workspace=None, status=None, stream=None):
+    """Attention of the last q_tokens tokens of every sequence over the
+    cache: q [batch, q_tokens, q_heads, head_dim] (bf16 or fp32; a token
+    stride is kept), page_table int32 [batch, width], seq_lens int32 [batch]
+    (new tokens counted, already written), scale 1/sqrt(head_dim) by default,
+    window 0 = all earlier tokens.  Returns (out, lse [batch, q_tokens,
+    q_heads] fp32)."""
+    if q.dim() != 4 or q.shape[3] != cache.head_dim:
+        raise ValueError(f"q: [batch, q_tokens, q_heads, {cache.head_dim}] required, got {list(q.shape)}")
+    B, L, HQ, D = q.shape
+    _cuda(page_table, "page_table", torch.int32)
+    _cuda(seq_lens, "seq_lens", torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape != (B,):
+        raise ValueError(f"page_table [{B}, width] and seq_lens [{B}] required")
+    if not page_table.is_contiguous() or not seq_lens.is_contiguous():
+        raise ValueError("page_table and seq_lens: contiguous tensors required")
+    if q.numel():
+        one = q.stride(1) if L > 1 else q.stride(0) if B > 1 else HQ * D
+        if q.stride(3) != 1 or (HQ > 1 and q.stride(2) != D) or (B > 1 and q.stride(0) != one * L):
+            raise ValueError("q: contiguous heads and elements and one stride from token to token required")
+    else:
+        one = HQ * D
+    out = torch.empty((B, L, HQ, D), dtype=q.dtype, device=q.device) if out is None else out
+    lse = torch.empty((B, L, HQ), dtype=torch.float32, device=q.device) if lse is None else lse
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out: contiguous, with q's shape and dtype")
+    if lse.shape != (B, L, HQ) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse: contiguous float32 [batch, q_tokens, q_heads]")
+    ws = workspace if workspace is not None else kv_attention_workspace(q, cache, page_table)
+    st = status if status is not None else cache.status
+    _same_device(cache.device, q, page_table, seq_lens, out, lse, ws, st)
+    with _on(cache.device):
+        _check(lib().fp4_kv_attention(cache._ref, _p(q), _dtype_code(q), B, L, HQ, one, _p(page_table),
+                                      page_table.shape[1], _p(seq_lens), D ** -0.5 if scale is None else scale,
+                                      window, _p(out), _p(lse), _p(ws), ws.numel() * ws.element_size(), _p(st),
+                                      _stream(stream)), "fp4_kv_attention")
+    return out, lse
+
+
+class LinearWeight:
+    """An FP4 weight [n, k] laid out for `linear`: packed codes [n, Kp/2]
+    (padded layout), the scale bytes in the MMA layout, the NVFP4 global
+    scale (None for MXFP4).  `status` as for KVCache."""
+
+    def __init__(self, fmt, packed, scales_mma, global_scale, n: int, k: int, status=None):
+        group = 16 if fmt == NVFP4 else 32
+        kp = _padded(k, group)
+        if fmt not in (NVFP4, MXFP4):
+            raise ValueError("fmt: NVFP4 or MXFP4")
+        dev = _cuda(packed, "packed", torch.uint8).device
+        _cuda(scales_mma, "scales_mma", torch.uint8)
+        if packed.numel() != n * kp // 2 or not packed.is_contiguous():
+            raise ValueError(f"packed: contiguous [{n}, {kp // 2}] required")
+        if scales_mma.numel() != lib().fp4_mma_scales_bytes(n, kp // group) or not scales_mma.is_contiguous():
+            raise ValueError("scales_mma: the MMA layout of the [n, Kp/G] scales required (scales_to_mma)")
+        if fmt == NVFP4 and (global_scale is None or global_scale.dtype != torch.float32 or global_scale.numel() != 1):
+            raise ValueError("global_scale: one float32 required for NVFP4")
+        _same_device(dev, scales_mma, global_scale, status)
+        self.fmt, self.n, self.k, self.device = fmt, n, k, dev
+        self.packed, self.scales_mma, self.global_scale = packed, scales_mma, global_scale
+        self.status = status if status is not None else new_status(dev)
+
+    def check(self, where: str = "LinearWeight"):
+        st = int(self.status.item())
+        if st != OK:
+            raise FP4Error(st, where)
+        return self
+
+
+def linear_weight(q: Quantized, stream=None) -> LinearWeight:
+    """The quantised weight [n, k] (nvfp4_quantize, mxfp4_quantize, the
+    padded and column-wise layouts, ...) laid out for `linear`, once."""
+    return LinearWeight(q.fmt, q.packed, scales_to_mma(q.scales, stream), q.global_scale, q.rows, q.cols)
+
+
+def linear_workspace(rows: int, w: LinearWeight) -> torch.Tensor:
+    """A workspace for `linear` calls of up to `rows` rows with w."""
+    return torch.empty(max(lib().fp4_linear_workspace_bytes(rows, w.k), 16), dtype=torch.uint8, device=w.device)
+
+
+def linear(x: torch.Tensor, w: LinearWeight, out_dtype=None, out=None, workspace=None, status=None,
+           stream=None) -> torch.Tensor:
+    """y [..., n] = x [..., k] W^T for a few rows of unquantised activations
+    (bf16 or fp32; rows of a 2-D x may be strided) and an FP4 weight.
+    out_dtype: x's by default."""
+    if x.dim() == 0 or x.shape[-1] != w.k:
+        raise ValueError(f"x: [..., {w.k}] required, got {list(x.shape)}")
+    rows = x.numel() // w.k if w.k else x.shape[:-1].numel()
+    if x.dim() == 2 and (x.stride(1) == 1 or w.k <= 1):
+        stride = x.stride(0) if rows > 1 else w.k
+    elif x.is_contiguous():
+        stride = w.k
+    else:
+        raise ValueError("x: contiguous elements required, and contiguous rows beyond two dimensions")
+    shape = (*x.shape[:-1], w.n)
+    y = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device) if out is None else out
+    if y.shape != shape or not y.is_contiguous():
+        raise ValueError(f"out: contiguous {list(shape)} required")
+    ws = workspace if workspace is not None else linear_workspace(rows, w)
+    st = status if status is not None else w.status
+    _same_device(w.device, x, y, ws, st)
+    with _on(w.device):
+        _check(lib().fp4_linear(w.fmt, _p(x), _dtype_code(x), rows, w.k, stride, _p(w.packed), _p(w.scales_mma),
+                                _p(w.global_scale), w.n, _p(y), _dtype_code(y), _p(ws),
+                                ws.numel() * ws.element_size(), _p(st), _stream(stream)), "fp4_linear")
+    return y
 
 
 def scale_search(x: torch.Tensor, with_loss: bool = True, workspace=None, status=None, stream=None,

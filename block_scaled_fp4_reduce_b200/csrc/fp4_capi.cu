@@ -143,11 +143,12 @@ const char *fp4_status_string(int status)
     case FP4_ERR_WORKSPACE: return "workspace missing or too small";
     case FP4_ERR_CUDA: return "CUDA launch failure";
     case FP4_ERR_TIMEOUT: return "a bounded device wait ran out";
+    case FP4_ERR_INDEX: return "slot, page or length out of range";
     default: return "unknown status";
     }
 }
 
-int fp4_version(void) { return 100; }
+int fp4_version(void) { return 101; }
 
 fp4_status fp4_set_launch_unit_limit(int64_t units)
 {

@@ -44,6 +44,7 @@ constexpr uint32_t kNonFiniteBits = 0x7F800000u;
 // Status values written to the caller's device status word (fp4.h).
 constexpr int32_t kStatusNonFinite = 4;
 constexpr int32_t kStatusRange = 5;
+constexpr int32_t kStatusIndex = 9;
 
 __device__ __forceinline__ void raise_status(int32_t *status, int32_t code)
 {

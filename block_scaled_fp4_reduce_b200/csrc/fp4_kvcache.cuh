@@ -1,0 +1,180 @@
+// fp4_kvcache.cuh -- keys and values quantised as they are written into a
+// paged FP4 cache, and read back.
+//
+// A cache page holds its tokens head by head: [heads, page_size, D/2] codes
+// and [heads, page_size, D/G] scale bytes, so that the tokens of one head,
+// which attention reads together, are contiguous.  Per block of G elements
+// the codec is the quantisers' (fp4_kernels.cuh): NVFP4 under the head's
+// global scale, MXFP4 by either scale rule; reading back is fp4_dequantize's
+// arithmetic.  Both directions are one pass over the data.
+#pragma once
+
+#include <cstdint>
+
+#include "fp4_kernels.cuh"
+
+namespace fp4 {
+
+// The cache as the kernels take it; `sel` 0 = keys, 1 = values.
+struct KvCache {
+    uint8_t *packed[2], *scales[2];
+    const float *g[2];
+    int64_t slots; // num_pages * page_size
+    int heads, blocks, page; // blocks of a token's head: head_dim / G
+};
+
+// Row (token of one head) of a slot.
+__device__ __forceinline__ int64_t kv_row(const KvCache &c, int64_t slot, int head)
+{
+    const int64_t page = slot / c.page;
+    return (page * c.heads + head) * c.page + (slot - page * c.page);
+}
+
+// The share of one thread: a unit is one block of one head of the keys or
+// of the values, and a thread keeps one unit for all its tokens, so that
+// what depends on the head (the double reciprocal of 6 g above all) is
+// formed once.  `per` units side by side in a CTA, kThreads / per tokens;
+// blockIdx.y walks units beyond kThreads.
+struct KvUnit {
+    int sel, head, block;
+    int64_t first; // its first token
+    int step;      // tokens between its tokens
+    bool any;
+};
+
+__device__ __forceinline__ KvUnit kv_unit(const KvCache &c, int units_of_row, int per)
+{
+    KvUnit u;
+    const int lane = (int)threadIdx.x % per, tok = (int)threadIdx.x / per;
+    const int per_cta = kThreads / per;
+    const int i = (int)blockIdx.y * per + lane; // keys' units, then the values'
+    const int one = c.heads * units_of_row;
+    u.any = tok < per_cta && i < 2 * one;
+    u.sel = i >= one;
+    const int j = i - (u.sel ? one : 0);
+    u.head = j / units_of_row;
+    u.block = j - u.head * units_of_row;
+    u.first = (int64_t)blockIdx.x * per_cta + tok;
+    u.step = (int)gridDim.x * per_cta;
+    return u;
+}
+
+// ---------------------------------------------------------------------------
+// Write.  One thread per block (32-byte loads, one packed store, one scale
+// byte), kKvTokens tokens in flight.
+// ---------------------------------------------------------------------------
+constexpr int kKvTokens = 2;
+
+template <typename T, bool kNv, bool kCeil>
+__global__ void __launch_bounds__(kThreads)
+    kv_write_kernel(const KvCache c, const T *__restrict__ k, const T *__restrict__ v, int64_t k_stride,
+                    int64_t v_stride, const int64_t *__restrict__ slots, int64_t tokens, int per, int32_t *status)
+{
+    constexpr int G = kNv ? 16 : 32;
+    pdl_begin();
+    const KvUnit u = kv_unit(c, c.blocks, per);
+    if (!u.any)
+        return;
+    NvScaleConsts sc = {};
+    if constexpr (kNv) {
+        const float g = __ldcg(c.g[u.sel] + u.head);
+        // 448 g has to be finite, and a subnormal g has no usable reciprocal
+        if (!(g >= 0x1p-126f && g <= 3.4028234663852886e38f / 2688.0f)) {
+            raise_status(status, kStatusRange);
+            return;
+        }
+        sc = nv_scale_consts(g);
+    }
+    const T *x = (u.sel ? v : k) + (int64_t)(u.head * c.blocks + u.block) * G;
+    const int64_t stride = u.sel ? v_stride : k_stride;
+    uint8_t *const packed = c.packed[u.sel], *const scales = c.scales[u.sel];
+    int32_t err = 0;
+    for (int64_t t = u.first; t < tokens; t += (int64_t)kKvTokens * u.step) {
+        Blk<T, G> blk[kKvTokens];
+        int64_t slot[kKvTokens];
+#pragma unroll
+        for (int i = 0; i < kKvTokens; ++i) {
+            const int64_t ti = t + (int64_t)i * u.step;
+            slot[i] = -1;
+            if (ti < tokens) {
+                slot[i] = __ldcg(slots + ti);
+                if (slot[i] >= c.slots) {
+                    err = kStatusIndex;
+                    slot[i] = -1;
+                }
+                load_blk(x + ti * stride, 0, blk[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kKvTokens; ++i) {
+            if (slot[i] < 0)
+                continue;
+            const int64_t at = kv_row(c, slot[i], u.head) * c.blocks + u.block;
+            if constexpr (kNv) {
+                if (absmax_bits(blk[i]) >= kNonFiniteBits)
+                    err = kStatusNonFinite;
+                nv_quantize_block(blk[i], sc, reinterpret_cast<uint2 *>(packed) + at, scales + at);
+            } else {
+                bool bad = false;
+                mx_quantize_block<kCeil>(blk[i], reinterpret_cast<uint4 *>(packed) + at, scales + at, bad);
+                if (bad)
+                    err = kStatusNonFinite;
+            }
+        }
+    }
+    if (err)
+        raise_status(status, err);
+}
+
+// ---------------------------------------------------------------------------
+// Read back.  One thread per 16 codes (8 packed bytes, one scale byte, 16
+// outputs), as the dequantiser.
+// ---------------------------------------------------------------------------
+template <typename T, bool kNv>
+__global__ void __launch_bounds__(kThreads)
+    kv_read_kernel(const KvCache c, T *__restrict__ k, T *__restrict__ v, int64_t k_stride, int64_t v_stride,
+                   const int64_t *__restrict__ slots, int64_t tokens, int per, int32_t *status)
+{
+    pdl_begin();
+    const int units = kNv ? c.blocks : 2 * c.blocks; // 16-code units of a row
+    const KvUnit u = kv_unit(c, units, per);
+    if (!u.any)
+        return;
+    const float g = kNv ? __ldcg(c.g[u.sel] + u.head) : 1.0f;
+    const uint64_t g2 = pack2(g, g);
+    T *y = (u.sel ? v : k) + (int64_t)(u.head * units + u.block) * 16;
+    const int64_t stride = u.sel ? v_stride : k_stride;
+    const uint2 *const packed = reinterpret_cast<const uint2 *>(c.packed[u.sel]);
+    const uint8_t *const scales = c.scales[u.sel];
+    bool bad = false;
+    for (int64_t t = u.first; t < tokens; t += (int64_t)kKvTokens * u.step) {
+        uint2 pk[kKvTokens];
+        uint32_t sbyte[kKvTokens];
+#pragma unroll
+        for (int i = 0; i < kKvTokens; ++i) {
+            const int64_t ti = t + (int64_t)i * u.step;
+            pk[i] = make_uint2(0u, 0u); // zeros where there is nothing to read
+            sbyte[i] = kNv ? 0u : 127u;
+            if (ti < tokens) {
+                const int64_t slot = __ldcg(slots + ti);
+                if (slot >= c.slots) {
+                    bad = true;
+                } else if (slot >= 0) {
+                    const int64_t at = kv_row(c, slot, u.head) * units + u.block;
+                    pk[i] = __ldcg(packed + at);
+                    sbyte[i] = __ldcg(scales + (kNv ? at : at >> 1));
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kKvTokens; ++i) {
+            const int64_t ti = t + (int64_t)i * u.step;
+            if (ti < tokens)
+                dequant_unit<kNv>(pk[i], sbyte[i], g2, y + ti * stride);
+        }
+    }
+    if (bad)
+        raise_status(status, kStatusIndex);
+}
+
+} // namespace fp4

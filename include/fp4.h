@@ -72,7 +72,8 @@ typedef enum fp4_status {
     FP4_ERR_RANGE = 5,       /* (device status) NVFP4 global scale out of range */
     FP4_ERR_WORKSPACE = 6,   /* workspace NULL or smaller than required */
     FP4_ERR_CUDA = 7,        /* a CUDA launch or query failed */
-    FP4_ERR_TIMEOUT = 8      /* (device status) a bounded wait on a copy ran out */
+    FP4_ERR_TIMEOUT = 8,     /* (device status) a bounded wait on a copy ran out */
+    FP4_ERR_INDEX = 9        /* (device status) a slot, page or length out of range */
 } fp4_status;
 
 typedef enum fp4_dtype { FP4_F32 = 0, FP4_BF16 = 1 } fp4_dtype;
@@ -452,6 +453,120 @@ fp4_status fp4_mxfp4_quantize_ceil_grouped(const fp4_quant_item *items, int n_it
  * items or 2^30 units of 16 codes. */
 fp4_status fp4_dequantize_grouped(fp4_format fmt, const fp4_dequant_item *items, int n_items,
                                   fp4_dtype out_dtype, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Single-token serving: a paged FP4 cache of keys and values, attention over
+ * it, and the product of a few rows of unquantised activations with an FP4
+ * weight.
+ *
+ * The cache.  Keys and values of `heads` KV heads of `head_dim` elements a
+ * token, in pages of `page_size` tokens, head by head inside a page:
+ *   k_packed, v_packed  uint8 [num_pages, heads, page_size, head_dim/2]
+ *   k_scales, v_scales  uint8 [num_pages, heads, page_size, head_dim/G]
+ * with codes, scale bytes and blocks along head_dim exactly as the
+ * quantisers above write them (G = 16 NVFP4, 32 MXFP4).  An NVFP4 cache has
+ * one global scale per head (fp32 [heads], the dequant multiplier g), fixed
+ * while the cache lives: a cache grows, so its amax is not known when its
+ * first token is written.  A value beyond 2688 g saturates.  MXFP4: the
+ * global scales are unused and may be NULL.
+ *   packed and scales 16-byte aligned (else FP4_ERR_ALIGN);
+ *   page_size a multiple of 16, head_dim of 32, at most 1024, heads *
+ *   head_dim at most 2^20 and num_pages * page_size at most 2^40 (else
+ *   FP4_ERR_SHAPE).
+ * Token position j of a sequence lies in slot page_table[j / page_size] *
+ * page_size + j % page_size.
+ * ------------------------------------------------------------------------ */
+typedef struct fp4_kv_cache {
+    fp4_format format;
+    int32_t heads, head_dim, page_size;
+    int64_t num_pages;
+    uint8_t *k_packed, *k_scales, *v_packed, *v_scales;
+    const float *k_global_scale, *v_global_scale; /* NVFP4: fp32 [heads] */
+} fp4_kv_cache;
+
+/* Quantise `tokens` tokens' keys and values into their cache slots.  k, v:
+ * [tokens, heads, head_dim], heads and elements contiguous, k_stride /
+ * v_stride elements from token to token (views of one fused projection);
+ * base and stride whole 32-byte vectors (else FP4_ERR_ALIGN), the strides at
+ * least heads * head_dim (else FP4_ERR_SHAPE).  slots: int64 [tokens]; a
+ * negative slot is a padding token, which is skipped; a slot past the cache
+ * sets INDEX and is skipped.  The slots of a call must differ: where two
+ * tokens name one slot it is unspecified whose blocks it holds.  Everything
+ * else in the cache is left as it was.
+ * Per block as fp4_nvfp4_quantize_with_amax with the head's g, or
+ * fp4_mxfp4_quantize with scale rule `rule` (ignored for NVFP4).  Data
+ * errors: NONFINITE (a NaN or Inf in a written token; its slot's content is
+ * then unspecified, the other slots' is not), RANGE (an NVFP4 global scale
+ * that is not a normal positive fp32; that head's content is left as it
+ * was), INDEX.  One kernel. */
+fp4_status fp4_kv_write(const fp4_kv_cache *cache, const void *k, const void *v, fp4_dtype dtype, int64_t tokens,
+                        int64_t k_stride, int64_t v_stride, const int64_t *slots, fp4_mx_rule rule, int32_t *status,
+                        cudaStream_t stream);
+
+/* Read slots back: k, v [tokens, heads, head_dim] of out_dtype (laid out as
+ * for fp4_kv_write), the values fp4_dequantize gives.  A negative slot gives
+ * zeros; a slot past the cache gives zeros and sets INDEX.  One kernel. */
+fp4_status fp4_kv_read(const fp4_kv_cache *cache, const int64_t *slots, int64_t tokens, void *k, void *v,
+                       fp4_dtype out_dtype, int64_t k_stride, int64_t v_stride, int32_t *status,
+                       cudaStream_t stream);
+
+/* Attention of q_tokens new tokens of each of `batch` sequences over the
+ * cache, which holds them already.  With x^ the dequantised keys and values,
+ * query token i of a sequence of n = seq_lens[b] tokens stands at position
+ * p = n - q_tokens + i and sees the positions j with 0 <= j <= p and, for
+ * window > 0, j > p - window:
+ *   x_j = softmax_scale * q . k^_j,  lse = log sum_j exp x_j,
+ *   out = sum_j exp(x_j - lse) v^_j.
+ * A token that sees nothing (p < 0, an empty sequence) gets out = 0 and
+ * lse = -inf.
+ *   q    [batch, q_tokens, q_heads, head_dim] bf16 or fp32, q_stride elements
+ *        from token to token (base and stride whole 16-byte vectors, else
+ *        FP4_ERR_ALIGN); q_heads a multiple of the cache's heads, head h of q
+ *        reads KV head h / (q_heads / heads)
+ *   out  as q, contiguous and 16-byte aligned; lse fp32 [batch, q_tokens,
+ *        q_heads] or NULL
+ *   page_table  int32 [batch, table_width]; seq_lens int32 [batch]
+ * head_dim 64, 128 or 256 (else FP4_ERR_SHAPE); softmax_scale finite.
+ * A length below 0 or above table_width * page_size sets INDEX, as does a
+ * page outside the cache that a visible position names; that sequence's
+ * outputs are then unspecified, the others' are not.  A NaN or Inf in a
+ * query sets NONFINITE, with that token's outputs unspecified.  Scores,
+ * softmax statistics and sums are fp32, q and the softmax weights enter the
+ * tensor cores as fp16 (two terms of it for fp32 q).  MXFP4: inside one token
+ * and head, what a block holds below 2^-24 of the head's largest block scale
+ * is rounded off.
+ * Written for few new tokens: the cache is read once for every 16 rows of
+ * q_tokens * q_heads / heads (8 for head_dim 256 or fp32 q); a long prompt reads it back with fp4_kv_read for
+ * a dense attention.  One kernel; the workspace must be zero-filled once
+ * before its first use, and every call leaves its counters at zero. */
+size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache *cache, int64_t batch, int64_t q_tokens, int64_t q_heads,
+                                        int64_t table_width);
+fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const void *q, fp4_dtype dtype, int64_t batch,
+                            int64_t q_tokens, int64_t q_heads, int64_t q_stride, const int32_t *page_table,
+                            int64_t table_width, const int32_t *seq_lens, float softmax_scale, int64_t window,
+                            void *out, float *lse, void *workspace, size_t workspace_bytes, int32_t *status,
+                            cudaStream_t stream);
+
+/* y [rows, N] = x W^^T for a few rows of unquantised activations x [rows, K]
+ * (bf16 or fp32) and the FP4 weight W^ [N, K] that packed / scales_mma /
+ * global_scale stand for (NVFP4 p s_b g, MXFP4 p 2^e).
+ *   packed      uint8 [N, Kp/2], Kp = K rounded up to whole blocks (the padded
+ *               layout); Kp a multiple of 32 (else FP4_ERR_SHAPE); 16-byte aligned
+ *   scales_mma  fp4_scales_to_mma_layout of the [N, Kp/G] scales, 16-byte aligned
+ *   x           x_stride elements from row to row, element aligned
+ *   y           out_dtype, contiguous, element aligned
+ * The activations enter the tensor cores as fp16 after a power of two per
+ * row (fp32 x as two terms, 22 bits): bf16 x is exact but for what lies
+ * below 2^-38 of its row's largest value.  Products are summed in fp32.
+ * A NaN or Inf in x sets NONFINITE (its row of y is then unspecified, the
+ * others are not).  N, K, rows below 2^31.  rows or N = 0: nothing is done;
+ * K = 0: y = 0.  Reads the weight once for every 64 rows (32 for fp32 x).  Two kernels;
+ * the workspace (any contents) holds the laid-out activations. */
+size_t fp4_linear_workspace_bytes(int64_t rows, int64_t K);
+fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t rows, int64_t K, int64_t x_stride,
+                      const uint8_t *packed, const uint8_t *scales_mma, const float *global_scale, int64_t N, void *y,
+                      fp4_dtype out_dtype, void *workspace, size_t workspace_bytes, int32_t *status,
+                      cudaStream_t stream);
 
 /* Tests only: the largest number of work units one launch takes (default
  * 2^30, restored by units = 0; else a multiple of 64 from 64 up).  Every
