@@ -2,14 +2,50 @@
 //
 //   x_j = scale q . k^_j,  m = max_j x_j,  out = sum_j e^(x_j - m) v^_j / sum_j e^(x_j - m)
 //
-// One warp per query row (sequence, new token, query head): its lanes share
-// the head's elements, the tokens run one after the other with the running
-// maximum and sum of the softmax in registers, so the scores are never
-// stored.
+// The query rows that read one KV head (new tokens x query heads of the
+// group) form a tile of 8 NT rows.  Grid: one CTA per (sequence, KV head, row
+// tile, split of the tokens); its kAttnWarps warps take steps of 32 tokens in
+// turn, each warp on its own -- own ring of staged steps (cp.async, kStages
+// deep), own running maximum, sum and output -- and meet once, at the end.
+// One pass over the cache; scores live in registers.
+//
+// Tensor cores (mma.sync m16n8k16, fp16 in, fp32 out): the cached side is the
+// M operand, so 16 tokens (or 16 elements of the head) meet 8 query rows per
+// instruction and a group of 1 to 8 query heads wastes no rows.
+//   scores   S^T [token, row] = K^ Q^T.  Lane (g, t) = (lane / 4, lane % 4)
+//            reads tokens g and g + 8 of a 16-token tile, elements t D/4 ..
+//            (t + 1) D/4 of each: contiguous codes, decoded to fp16 pairs and
+//            scaled by the block's scale (code x E4M3 scale is exact in fp16).
+//            Which element is which k index is free as long as Q's operand
+//            agrees, so nothing is shuffled.
+//   output   O^T [element, row] += V^T P^T.  Lane (g, t) reads elements g D/8
+//            .. (g + 1) D/8 of tokens 2t, 2t + 1, 2t + 8, 2t + 9; the codes of
+//            two tokens are interleaved nibble by nibble before they are
+//            decoded, which gives the (token, token + 1) pairs of the operand
+//            directly.  P comes out of the score tiles transposed by
+//            movmatrix.
+// Query rows enter as fp16 after a power of two that brings the row's maximum
+// to 2^14 (exact for bf16 but for elements 2^-38 below the maximum); fp32
+// rows as two fp16 terms.  Softmax weights enter as fp16 scaled by 2^15, so
+// that weights down to 2^-29 of the largest keep all their bits and the rest
+// down to 2^-39 some; fp32 calls add a second term.
+//
+// MXFP4: a block scale 2^e does not fit fp16.  Inside a token the scales are
+// taken relative to the token's largest, 2^(e - E) (0 below 2^-24); 2^E of a
+// key multiplies the finished score in fp32, 2^E of a value joins the softmax
+// weight: the weights' own reference is m' = max_j (x_j + E_j), beside the
+// softmax's m, so that no value, however large or small, pushes another's
+// weight out of fp16's range.
+//
+// What bounds it: 0.5625 bytes per cached element (NVFP4) against about 2.5
+// instructions per element and lane group for decoding, so HBM and the issue
+// slots are within a factor of two of each other; steps of 32 tokens amortise
+// the softmax.
 #pragma once
 
 #include <cstdint>
 
+#include "fp4_async.cuh"
 #include "fp4_kvcache.cuh"
 
 namespace fp4 {
@@ -17,96 +53,771 @@ namespace fp4 {
 struct AttnArgs {
     KvCache c;
     const void *q;
-    int batch, q_tokens, q_heads, head_dim;
+    int batch, q_tokens, q_heads;
+    int group, rows, row_tiles, splits, chunk; // rows = q_tokens * group; chunk: tokens of a split
     int64_t q_stride;
     const int32_t *page_table;
-    int64_t table_width, window;
+    int table_width;
+    int64_t capacity, window; // table_width * page
+    uint64_t page_magic;      // 2^64 / (page / 16), rounded up
     const int32_t *seq_lens;
-    float scale;
+    float scale; // softmax scale * log2(e)
     void *out;
     float *lse;
+    float *partial;  // [unit][split][8 NT][D] outputs of a split, unnormalised
+    float4 *stats;   // [unit][split][8 NT] m, l, m'
     int32_t *status;
 };
 
-template <typename T> __device__ __forceinline__ float to_f32(T v)
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnStep = 32;       // tokens of a warp's step
+constexpr float kAttnBias = 15.0f;  // weights enter the tensor cores times 2^15
+constexpr float kLn2 = 0.693147180559945309f;
+
+template <int D> constexpr int kAttnStages = D == 64 ? 4 : D == 128 ? 3 : 2;
+
+// Bytes of one staged step: codes and scale bytes of 32 tokens' keys and values.
+template <bool kNv, int D> constexpr int kAttnStageBytes = 2 * kAttnStep * (D / 2 + D / (kNv ? 16 : 32));
+
+template <bool kNv, int D, int NT> constexpr int attn_smem()
 {
-    if constexpr (sizeof(T) == 2)
-        return __uint_as_float((uint32_t)v << 16);
-    else
-        return v;
+    const int ring = kAttnWarps * kAttnStages<D> * kAttnStageBytes<kNv, D>;
+    const int merge = kAttnWarps * 8 * NT * (D + 4) * 4;
+    return ring > merge ? ring : merge;
 }
 
-// One element of a cached row: code, block scale, global scale.
-template <bool kNv> __device__ __forceinline__ float kv_value(const KvCache &c, int sel, int64_t row, int d, float g)
+__device__ __forceinline__ float ex2(float x)
 {
-    constexpr int G = kNv ? 16 : 32;
-    const uint32_t byte = __ldcg(c.packed[sel] + row * (c.blocks * G / 2) + d / 2);
-    float lo, hi;
-    f16x2_to_f32(e2m1x2_to_f16x2(byte), lo, hi);
-    const uint32_t s = __ldcg(c.scales[sel] + row * c.blocks + d / G);
-    return __fmul_rn(__fmul_rn((d & 1) ? hi : lo, kNv ? e4m3_to_f32(s) : e8m0_to_f32(s)), g);
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-template <typename T, bool kNv> __global__ void __launch_bounds__(kThreads) kv_attention_kernel(const AttnArgs a)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
 {
-    pdl_begin();
-    constexpr int kMost = 256 / 32; // elements of a lane
-    const int lane = (int)threadIdx.x & 31;
-    const int64_t rows = (int64_t)a.batch * a.q_tokens * a.q_heads;
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (row >= rows)
-        return;
-    const int h = (int)(row % a.q_heads);
-    const int64_t bi = row / a.q_heads;
-    const int i = (int)(bi % a.q_tokens), b = (int)(bi / a.q_tokens);
-    const int kvh = h / (a.q_heads / a.c.heads), per = a.head_dim / 32;
-    const T *q = static_cast<const T *>(a.q) + bi * a.q_stride + (int64_t)h * a.head_dim;
-    float qv[kMost], o[kMost];
-    bool bad = false;
-    for (int e = 0; e < kMost; ++e) {
-        qv[e] = e < per ? to_f32(__ldcg(q + e * 32 + lane)) : 0.0f;
-        bad |= (__float_as_uint(qv[e]) & 0x7FFFFFFFu) >= kNonFiniteBits;
-        o[e] = 0.0f;
-    }
-    if (bad)
-        raise_status(a.status, kStatusNonFinite);
-    const float gk = kNv ? __ldcg(a.c.g[0] + kvh) : 1.0f, gv = kNv ? __ldcg(a.c.g[1] + kvh) : 1.0f;
-    int64_t n = __ldcg(a.seq_lens + b);
-    if (n < 0 || n > a.table_width * a.c.page) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// (lo, hi) -> f16x2, round to nearest even.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// The two E4M3 bytes in the low half of v as an f16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// 2^-d as f16 bits, d >= 0: normal to d = 14, subnormal to 24, then 0.
+__device__ __forceinline__ uint32_t f16_exp2_neg(int d)
+{
+    return d <= 14 ? (uint32_t)(15 - d) << 10 : (d <= 24 ? 1u << (24 - d) : 0u);
+}
+
+// Largest of the four bytes of v.
+__device__ __forceinline__ uint32_t max_byte(uint32_t v)
+{
+    const uint32_t a = max(v & 0xFFu, (v >> 8) & 0xFFu), b = max((v >> 16) & 0xFFu, v >> 24);
+    return max(a, b);
+}
+
+// Positions that a row tile needs, and its splits: tokens [lo, hi], staged
+// from `base` (lo rounded down to 16) in `ns` splits of `chunk` tokens.
+struct AttnSpan {
+    int n, lo, hi, base, ns;
+};
+
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int b, int first_token, int last_token)
+{
+    AttnSpan s;
+    s.n = __ldcg(a.seq_lens + b);
+    if (s.n < 0 || s.n > a.capacity) {
         raise_status(a.status, kStatusIndex);
-        n = 0;
+        s.n = 0;
     }
-    const int64_t p = n - a.q_tokens + i;
-    int64_t first = a.window > 0 ? p - a.window + 1 : 0;
-    first = first < 0 ? 0 : first;
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t j = first; j <= p; ++j) {
-        const int64_t page = __ldcg(a.page_table + b * a.table_width + j / a.c.page);
-        if (page < 0 || page >= a.c.slots / a.c.page) {
+    s.hi = s.n - a.q_tokens + last_token; // may be negative: nothing to see
+    const int p = s.n - a.q_tokens + first_token;
+    s.lo = a.window > 0 && p >= a.window ? p - (int)a.window + 1 : 0;
+    s.base = s.lo & ~15;
+    s.ns = s.hi < s.lo ? 0 : (s.hi - s.base) / a.chunk + 1;
+    return s;
+}
+
+// ---------------------------------------------------------------------------
+// TQ: uint16_t (bf16) or float.
+// ---------------------------------------------------------------------------
+template <typename TQ, bool kNv, int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnArgs a)
+{
+    constexpr int kParts = sizeof(TQ) == 4 ? 2 : 1; // fp16 terms of a query element and of a weight
+    constexpr int G = kNv ? 16 : 32, NB = D / G;    // scale bytes of a token
+    constexpr int kStages = kAttnStages<D>, kStage = kAttnStageBytes<kNv, D>;
+    constexpr int kCodes = kAttnStep * D / 2, kScales = kAttnStep * NB;
+    constexpr int KS = D / 16; // k steps of the scores = 16-element tiles of the output
+    constexpr int R = 8 * NT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) uint16_t s_q[kParts][R][D + 8];
+    __shared__ float s_exp[R]; // 2^(exponent taken out of the row)
+
+    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int unit = (int)blockIdx.x / a.splits, split = (int)blockIdx.x - unit * a.splits;
+    const int bh = unit / a.row_tiles, rt = unit - bh * a.row_tiles;
+    const int b = bh / a.c.heads, kvh = bh - b * a.c.heads;
+    const int row0 = rt * R, rows = min(R, a.rows - row0);
+    const int i0 = row0 / a.group; // new token of the first row
+    pdl_begin();
+    const AttnSpan sp = attn_span(a, b, i0, (row0 + rows - 1) / a.group);
+    if (split > 0 && split >= sp.ns)
+        return;
+
+    // this warp's steps: token tok0 + 32 (warp + 4 s), below `end`
+    const int tok0 = sp.base + split * a.chunk;
+    const int end = sp.ns == 0 ? tok0 : min(sp.hi + 1, tok0 + a.chunk);
+    const int steps_all = (end - tok0 + kAttnStep - 1) / kAttnStep;
+    const int steps = steps_all > warp ? (steps_all - warp + kAttnWarps - 1) / kAttnWarps : 0;
+    uint8_t *const ring = smem + warp * kStages * kStage;
+    const int32_t *const table = a.page_table + (int64_t)b * a.table_width;
+    const int page16 = a.c.page >> 4;
+    const int64_t pages = a.c.slots / a.c.page;
+
+    // 16-token granule `gr` (in 16-token units of the sequence): its page
+    // table entry, -1 when no token of it is needed.
+    auto entry = [&](int gr) -> int {
+        if (gr * 16 >= end)
+            return -1;
+        const int pi = page16 == 1 ? gr : (int)__umul64hi((uint64_t)(uint32_t)gr, a.page_magic);
+        const int e = __ldcg(table + pi);
+        if (e < 0 || e >= pages) {
             raise_status(a.status, kStatusIndex);
-            continue;
+            return -1;
         }
-        const int64_t at = kv_row(a.c, page * a.c.page + j % a.c.page, kvh);
-        float x = 0.0f;
-        for (int e = 0; e < kMost; ++e)
-            if (e < per)
-                x = fmaf(qv[e], kv_value<kNv>(a.c, 0, at, e * 32 + lane, gk), x);
-        for (int s = 16; s; s >>= 1)
-            x += __shfl_xor_sync(0xFFFFFFFFu, x, s);
-        x *= a.scale;
-        const float mn = fmaxf(m, x), alpha = expf(m - mn), w = expf(x - mn);
-        l = fmaf(l, alpha, w);
-        for (int e = 0; e < kMost; ++e)
-            if (e < per)
-                o[e] = fmaf(o[e], alpha, w * kv_value<kNv>(a.c, 1, at, e * 32 + lane, gv));
-        m = mn;
+        return e;
+    };
+    // Row (16 tokens of this head) of a granule, in units of tokens.
+    auto granule_row = [&](int gr, int e) -> int64_t {
+        const int pi = page16 == 1 ? gr : (int)__umul64hi((uint64_t)(uint32_t)gr, a.page_magic);
+        return ((int64_t)e * a.c.heads + kvh) * a.c.page + (int64_t)(gr - pi * page16) * 16;
+    };
+    // Copies of one step into a stage.  Chunks of 16 bytes: codes D / 32 per
+    // token, swizzled so that both operands' reads are free of bank
+    // conflicts; scales NB per granule.
+    auto issue = [&](int s, int e0, int e1) {
+        uint8_t *st = ring + (s % kStages) * kStage;
+        const uint32_t dst = smem_addr(st);
+        const int gr = (tok0 + kAttnStep * (warp + kAttnWarps * s)) >> 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = h ? e1 : e0;
+            if (e < 0)
+                continue;
+            const int64_t row = granule_row(gr + h, e);
+            constexpr int kPer = D / 32; // chunks of a token
+#pragma unroll
+            for (int i = 0; i < kPer / 2; ++i) { // 16 tokens: 16 kPer chunks
+                const int c = lane + 32 * i, tk = c / kPer, ch = c % kPer, r = h * 16 + tk;
+                const int64_t src = row * (D / 2) + c * 16;
+                const uint32_t kc = D == 256 ? (uint32_t)(r * kPer + (ch ^ (r & 1))) : (uint32_t)(r * kPer + ch);
+                uint32_t vc;
+                if constexpr (D == 64)
+                    vc = (uint32_t)(r * kPer + ch) ^ (((uint32_t)r >> 2 & 1) * 2);
+                else
+                    vc = (uint32_t)(r * kPer + ch) ^ (((uint32_t)r >> 1 & 3) * 2);
+                cp_async16(dst + kc * 16, a.c.packed[0] + src);
+                cp_async16(dst + kCodes + vc * 16, a.c.packed[1] + src);
+            }
+            // lanes below 2 NB: NB chunks of the keys' scales, then of the values'
+            const uint32_t sdst = dst + 2 * kCodes + h * 16 * NB;
+            if (lane < NB)
+                cp_async16(sdst + lane * 16, a.c.scales[0] + row * NB + lane * 16);
+            else if (lane < 2 * NB)
+                cp_async16(sdst + kScales + (lane - NB) * 16, a.c.scales[1] + row * NB + (lane - NB) * 16);
+        }
+    };
+
+    // fill the ring before anything else: the copies run under the query's preparation
+    const int gr0 = (tok0 >> 4) + 2 * warp;
+    constexpr int kGrStep = 2 * kAttnWarps; // granules between a warp's steps
+    int e0 = -1, e1 = -1;
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        if (s < steps)
+            issue(s, entry(gr0 + s * kGrStep), entry(gr0 + s * kGrStep + 1));
+        cp_async_commit();
     }
-    T *out = static_cast<T *>(a.out) + row * a.head_dim;
-    for (int e = 0; e < kMost; ++e)
-        if (e < per)
-            out[e * 32 + lane] = to_out<T>(l > 0.0f ? o[e] / l : 0.0f);
+    if (kStages - 1 < steps) {
+        e0 = entry(gr0 + (kStages - 1) * kGrStep);
+        e1 = entry(gr0 + (kStages - 1) * kGrStep + 1);
+    }
+
+    // Query rows to fp16: a warp takes rows warp, warp + 4, ...
+    for (int r = warp; r < R; r += kAttnWarps) {
+        float v[D / 32];
+        uint32_t top = 0;
+        const int i = (row0 + r) / a.group, h = kvh * a.group + (row0 + r) - i * a.group;
+        const TQ *q = static_cast<const TQ *>(a.q) + ((int64_t)b * a.q_tokens + i) * a.q_stride + (int64_t)h * D;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+            v[e] = 0.0f;
+            if (r < rows) {
+                if constexpr (sizeof(TQ) == 2)
+                    v[e] = __uint_as_float((uint32_t)__ldcg(q + e * 32 + lane) << 16);
+                else
+                    v[e] = __ldcg(q + e * 32 + lane);
+            }
+            top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        }
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if (top >= kNonFiniteBits && lane == 0)
+            raise_status(a.status, kStatusNonFinite);
+        // times 2^(14 - floor(log2 max)), in two exact steps; rows below 2^-112 count as if their maximum were that
+        int ex = max((int)(top >> 23), 15) - 127; // floor(log2 max)
+        if (top >= kNonFiniteBits)
+            ex = 14;
+        const float up = __uint_as_float((uint32_t)(127 + (14 - ex)) << 23);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+            const float x = v[e] * up;
+            const uint32_t hi = pack_f16x2(x, 0.0f) & 0xFFFFu;
+            s_q[0][r][e * 32 + lane] = (uint16_t)hi;
+            if constexpr (kParts == 2) {
+                float back, none;
+                f16x2_to_f32(hi, back, none);
+                s_q[1][r][e * 32 + lane] = (uint16_t)(pack_f16x2((x - back) * 2048.0f, 0.0f) & 0xFFFFu);
+            }
+        }
+        if (lane == 0)
+            s_exp[r] = __uint_as_float((uint32_t)(127 + (ex - 14)) << 23);
+    }
+    __syncthreads();
+    // Q's operand: lane (g, t) holds row g, elements t D/4 + 4 s .. + 3 of k step s
+    uint32_t qb[kParts][NT][KS][2];
+    float rowc[NT][2];     // score of rows 2t, 2t + 1 in units of log2
+    int last[NT][2], first[NT][2]; // their visible positions
+    const float gk = kNv ? __ldcg(a.c.g[0] + kvh) : 1.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(&s_q[p][n * 8 + g][t * (D / 4) + 4 * s]);
+                qb[p][n][s][0] = w.x;
+                qb[p][n][s][1] = w.y;
+            }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = n * 8 + 2 * t + e;
+            rowc[n][e] = a.scale * gk * s_exp[r];
+            last[n][e] = r < rows ? sp.n - a.q_tokens + (row0 + r) / a.group : -1;
+            first[n][e] = a.window > 0 ? last[n][e] - (int)min(a.window, (int64_t)0x40000000) + 1 : 0;
+        }
+    }
+
+    float o[NT][KS][4], m[NT][2], mw[NT][2], l[NT][2]; // mw: the weights' reference (MXFP4; m for NVFP4)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[n][i][e] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            m[n][e] = mw[n][e] = -INFINITY;
+            l[n][e] = 0.0f;
+        }
+    }
+
+    // every row of the tile sees all of [all_lo, all_hi]
+    const int all_lo = a.window > 0 ? max(0, sp.n - a.q_tokens + (row0 + rows - 1) / a.group - (int)min(a.window, (int64_t)0x40000000) + 1) : 0;
+    const int all_hi = sp.n - a.q_tokens + i0;
+
+    for (int s = 0; s < steps; ++s) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        if (s + kStages - 1 < steps)
+            issue(s + kStages - 1, e0, e1);
+        cp_async_commit();
+        e0 = e1 = -1;
+        if (s + kStages < steps) {
+            e0 = entry(gr0 + (s + kStages) * kGrStep);
+            e1 = entry(gr0 + (s + kStages) * kGrStep + 1);
+        }
+        uint8_t *const st = ring + (s % kStages) * kStage;
+        uint8_t *const ks = st + 2 * kCodes, *const vs = ks + kScales;
+        const int tok = tok0 + kAttnStep * (warp + kAttnWarps * s);
+        const bool edge = tok < all_lo || tok + kAttnStep - 1 > all_hi;
+        if (edge) { // scale bytes of tokens that no row sees may be anything: zero them
+            if (tok + lane < sp.lo || tok + lane > sp.hi) {
+#pragma unroll
+                for (int i = 0; i < NB; i += 2) {
+                    *reinterpret_cast<uint16_t *>(ks + lane * NB + i) = 0;
+                    *reinterpret_cast<uint16_t *>(vs + lane * NB + i) = 0;
+                }
+            }
+            __syncwarp();
+        }
+
+        // ---- scores: two tiles of 16 tokens ----
+        float x[NT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            float acc[kParts][NT][4];
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[p][n][e] = 0.0f;
+            float tokf[2]; // MXFP4: 2^E of tokens g, g + 8
+            constexpr int W = D / 32; // 32-bit words of a lane's codes of a token
+            uint32_t w[2][W], sc[2][D / 64]; // scale of each 16 elements, as an f16 pair
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int r = mt * 16 + u * 8 + g;
+                if constexpr (D == 64) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(st + r * 32 + t * 8);
+                    w[u][0] = v.x;
+                    w[u][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < W / 4; ++c) {
+                        const int ch = D == 256 ? (2 * t + c) ^ (r & 1) : t;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(st + r * (D / 2) + ch * 16);
+                        w[u][4 * c] = v.x;
+                        w[u][4 * c + 1] = v.y;
+                        w[u][4 * c + 2] = v.z;
+                        w[u][4 * c + 3] = v.w;
+                    }
+                }
+                if constexpr (kNv) {
+                    if constexpr (D == 64) {
+                        const uint32_t f = e4m3x2_to_f16x2(ks[r * NB + t]);
+                        sc[u][0] = __byte_perm(f, f, 0x1010);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < D / 128; ++c) {
+                            const uint32_t f = e4m3x2_to_f16x2(
+                                *reinterpret_cast<const uint16_t *>(ks + r * NB + t * (D / 64) + 2 * c));
+                            sc[u][2 * c] = __byte_perm(f, f, 0x1010);
+                            sc[u][2 * c + 1] = __byte_perm(f, f, 0x3232);
+                        }
+                    }
+                    tokf[u] = 1.0f;
+                } else {
+                    uint32_t lo4, top;
+                    if constexpr (D == 64) {
+                        lo4 = *reinterpret_cast<const uint16_t *>(ks + r * NB);
+                        top = max(lo4 & 0xFFu, lo4 >> 8);
+                        const int mine = (int)((lo4 >> (8 * (t >> 1))) & 0xFFu);
+                        sc[u][0] = f16_exp2_neg((int)top - mine) * 0x10001u;
+                    } else if constexpr (D == 128) {
+                        lo4 = *reinterpret_cast<const uint32_t *>(ks + r * NB);
+                        top = max_byte(lo4);
+                        sc[u][0] = sc[u][1] = f16_exp2_neg((int)top - (int)((lo4 >> (8 * t)) & 0xFFu)) * 0x10001u;
+                    } else {
+                        const uint2 both = *reinterpret_cast<const uint2 *>(ks + r * NB);
+                        top = max(max_byte(both.x), max_byte(both.y));
+                        const uint32_t mine = ((t & 2) ? both.y : both.x) >> (16 * (t & 1));
+                        sc[u][0] = sc[u][1] = f16_exp2_neg((int)top - (int)(mine & 0xFFu)) * 0x10001u;
+                        sc[u][2] = sc[u][3] = f16_exp2_neg((int)top - (int)((mine >> 8) & 0xFFu)) * 0x10001u;
+                    }
+                    tokf[u] = e8m0_to_f32(top);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k) { // word k / 2, its half k % 2: elements 4 k .. 4 k + 3
+                uint32_t f[2][2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        f[u][j] = f16x2_mul(e2m1x2_to_f16x2(w[u][k / 2] >> (16 * (k & 1) + 8 * j)), sc[u][k / 4]);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma_f16(acc[p][n], f[0][0], f[1][0], f[0][1], f[1][1], qb[p][n][k][0], qb[p][n][k][1]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v = acc[0][n][e];
+                    if constexpr (kParts == 2)
+                        v = fmaf(acc[1][n][e], 0x1p-11f, v);
+                    if constexpr (!kNv)
+                        v *= tokf[e >> 1];
+                    x[n][mt][e] = v * rowc[n][e & 1];
+                }
+        }
+        if (edge) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = tok + mt * 16 + (e >> 1) * 8 + g;
+                        if (j > last[n][e & 1] || j < first[n][e & 1])
+                            x[n][mt][e] = -INFINITY;
+                    }
+        }
+
+        // ---- softmax of the step ----
+        float ev[2][2]; // MXFP4: E of the values of token 16 mt + 8 u + g
+        if constexpr (!kNv) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint8_t *p = vs + (mt * 16 + u * 8 + g) * NB;
+                    uint32_t top;
+                    if constexpr (D == 64)
+                        top = max((uint32_t)p[0], (uint32_t)p[1]);
+                    else if constexpr (D == 128)
+                        top = max_byte(*reinterpret_cast<const uint32_t *>(p));
+                    else
+                        top = max(max_byte(*reinterpret_cast<const uint32_t *>(p)),
+                                  max_byte(*reinterpret_cast<const uint32_t *>(p + 4)));
+                    ev[mt][u] = (float)((int)top - 127);
+                }
+        }
+        bool changed = false;
+        float alpha[NT][2], ref[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float top = fmaxf(fmaxf(x[n][0][e], x[n][0][e + 2]), fmaxf(x[n][1][e], x[n][1][e + 2]));
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                const float mn = fmaxf(m[n][e], top);
+                if constexpr (kNv) {
+                    changed |= mn > mw[n][e];
+                    alpha[n][e] = mn > mw[n][e] ? ex2(mw[n][e] - mn) : 1.0f;
+                    l[n][e] *= alpha[n][e];
+                    mw[n][e] = mn;
+                } else {
+                    if (mn > m[n][e])
+                        l[n][e] *= ex2(m[n][e] - mn);
+                    float tw = fmaxf(fmaxf(x[n][0][e] + ev[0][0], x[n][0][e + 2] + ev[0][1]),
+                                     fmaxf(x[n][1][e] + ev[1][0], x[n][1][e + 2] + ev[1][1]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1)
+                        tw = fmaxf(tw, __shfl_xor_sync(0xFFFFFFFFu, tw, d));
+                    const float mwn = fmaxf(mw[n][e], tw);
+                    changed |= mwn > mw[n][e];
+                    alpha[n][e] = mwn > mw[n][e] ? ex2(mw[n][e] - mwn) : 1.0f;
+                    mw[n][e] = mwn;
+                }
+                m[n][e] = mn;
+                ref[n][e] = mn == -INFINITY ? 0.0f : mn; // a row that has seen nothing yet
+            }
+        if (__any_sync(0xFFFFFFFFu, changed)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[n][i][e] *= alpha[n][e & 1];
+        }
+        // weights of rows 2t, 2t + 1 for token g of each 8: transposed, they are the operand of row g
+        uint32_t pb[kParts][NT][2][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float p[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float xx = x[n][mt][2 * u + e];
+                        if constexpr (kNv) {
+                            p[e] = ex2(xx - (ref[n][e] - kAttnBias));
+                            l[n][e] += p[e];
+                        } else {
+                            l[n][e] += ex2(xx - (ref[n][e] - kAttnBias));
+                            p[e] = ex2(xx + ev[mt][u] - ((mw[n][e] == -INFINITY ? 0.0f : mw[n][e]) - kAttnBias));
+                        }
+                    }
+                    const uint32_t hi = pack_f16x2(p[0], p[1]);
+                    pb[0][n][mt][u] = transpose8x8(hi);
+                    if constexpr (kParts == 2) {
+                        float b0, b1;
+                        f16x2_to_f32(hi, b0, b1);
+                        pb[1][n][mt][u] = transpose8x8(pack_f16x2(p[0] - b0, p[1] - b1));
+                    }
+                }
+
+        // ---- output: two k steps of 16 tokens ----
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            constexpr int W = D / 64 ? D / 64 : 1; // words of a lane's codes of a token
+            uint32_t w[4][W];                      // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t r = (uint32_t)(mt * 16 + 2 * t + (c & 1) + (c >> 1) * 8);
+                const uint8_t *v = st + kCodes;
+                if constexpr (D == 64) {
+                    const uint32_t ch = (r * 2 + (g >> 2)) ^ ((r >> 2 & 1) * 2);
+                    w[c][0] = *reinterpret_cast<const uint32_t *>(v + ch * 16 + (g & 3) * 4);
+                } else if constexpr (D == 128) {
+                    const uint32_t ch = (r * 4 + (g >> 1)) ^ ((r >> 1 & 3) * 2);
+                    const uint2 x2 = *reinterpret_cast<const uint2 *>(v + ch * 16 + (g & 1) * 8);
+                    w[c][0] = x2.x;
+                    w[c][1] = x2.y;
+                } else {
+                    const uint32_t ch = (r * 8 + g) ^ ((r >> 1 & 3) * 2);
+                    const uint4 x4 = *reinterpret_cast<const uint4 *>(v + ch * 16);
+                    w[c][0] = x4.x;
+                    w[c][1] = x4.y;
+                    w[c][2] = x4.z;
+                    w[c][3] = x4.w;
+                }
+            }
+            // scale pairs (token, token + 1) of the lane's 16-element pieces
+            constexpr int SB = D >= 256 ? 2 : 1;
+            uint32_t sv[2][SB];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int r = mt * 16 + 2 * t + 8 * c;
+                const uint8_t *p0 = vs + r * NB, *p1 = p0 + NB;
+                if constexpr (kNv) {
+#pragma unroll
+                    for (int i = 0; i < SB; ++i) {
+                        const int at = D == 64 ? g >> 1 : SB * g + i;
+                        sv[c][i] = e4m3x2_to_f16x2((uint32_t)p0[at] | (uint32_t)p1[at] << 8);
+                    }
+                } else {
+                    uint32_t top0, top1;
+                    if constexpr (D == 64) {
+                        top0 = max((uint32_t)p0[0], (uint32_t)p0[1]);
+                        top1 = max((uint32_t)p1[0], (uint32_t)p1[1]);
+                    } else if constexpr (D == 128) {
+                        top0 = max_byte(*reinterpret_cast<const uint32_t *>(p0));
+                        top1 = max_byte(*reinterpret_cast<const uint32_t *>(p1));
+                    } else {
+                        top0 = max(max_byte(*reinterpret_cast<const uint32_t *>(p0)),
+                                   max_byte(*reinterpret_cast<const uint32_t *>(p0 + 4)));
+                        top1 = max(max_byte(*reinterpret_cast<const uint32_t *>(p1)),
+                                   max_byte(*reinterpret_cast<const uint32_t *>(p1 + 4)));
+                    }
+                    const int at = D == 64 ? g >> 2 : D == 128 ? g >> 1 : g;
+                    const uint32_t pair = f16_exp2_neg((int)top0 - (int)p0[at]) |
+                                          f16_exp2_neg((int)top1 - (int)p1[at]) << 16;
+#pragma unroll
+                    for (int i = 0; i < SB; ++i)
+                        sv[c][i] = pair;
+                }
+            }
+            // the lane's D / 8 elements: its first D / 16 are the low rows of
+            // the output tiles, its last D / 16 the high ones
+#pragma unroll
+            for (int j = 0; j < D / 16; j += 2) { // elements j, j + 1 of each half
+                uint32_t f[2][2][2]; // [half][token pair][element]
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int el = h * (D / 16) + j, word = el / 8, byte = (el % 8) / 2;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t w0 = w[2 * c][word], w1 = w[2 * c + 1][word];
+                        // byte: (token's element, next token's element)
+                        const uint32_t ev_ = (w0 & 0x0F0F0F0Fu) | ((w1 & 0x0F0F0F0Fu) << 4);
+                        const uint32_t od_ = ((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u);
+                        f[h][c][0] = f16x2_mul(e2m1x2_to_f16x2(ev_ >> (8 * byte)), sv[c][el / 16 % SB]);
+                        f[h][c][1] = f16x2_mul(e2m1x2_to_f16x2(od_ >> (8 * byte)), sv[c][el / 16 % SB]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16(o[n][j + i], f[0][0][i], f[1][0][i], f[0][1][i], f[1][1][i], pb[p][n][mt][0],
+                                    pb[p][n][mt][1]);
+            }
+        }
+    }
+    cp_async_wait<0>();
+
+    // ---- the warps' results, merged ----
+    float *const so = reinterpret_cast<float *>(smem); // [warp][row][D + 4]
+    __shared__ float4 s_stats[kAttnWarps][R];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float sum = l[n][e];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1)
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+            const int r = n * 8 + 2 * t + e;
+            if (g == 0)
+                s_stats[warp][r] = make_float4(m[n][e], sum, mw[n][e], 0.0f);
+            float *dst = so + ((warp * R) + r) * (D + 4) + g * (D / 8);
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                dst[i] = o[n][i][e];
+                dst[D / 16 + i] = o[n][i][e + 2];
+            }
+        }
+    __syncthreads();
+    const float gv = kNv ? __ldcg(a.c.g[1] + kvh) : 1.0f;
+    const bool whole = sp.ns <= 1;
+    for (int idx = (int)threadIdx.x; idx < rows * (D / 4); idx += kAttnThreads) {
+        const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
+        float mm = -INFINITY, mx = -INFINITY, ll = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            mm = fmaxf(mm, s_stats[w][r].x);
+            mx = fmaxf(mx, s_stats[w][r].z);
+        }
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            const float4 s = s_stats[w][r];
+            if (s.y > 0.0f) {
+                ll = fmaf(s.y, ex2(s.x - mm), ll);
+                const float f = ex2(s.z - mx);
+                const float4 p = *reinterpret_cast<const float4 *>(so + (w * R + r) * (D + 4) + d);
+                v.x = fmaf(p.x, f, v.x);
+                v.y = fmaf(p.y, f, v.y);
+                v.z = fmaf(p.z, f, v.z);
+                v.w = fmaf(p.w, f, v.w);
+            }
+        }
+        if (whole) {
+            // sums and weights both carry 2^bias; the values 2^(m' - m)
+            const int i = (row0 + r) / a.group;
+            const int64_t at = ((int64_t)b * a.q_tokens + i) * a.q_heads + kvh * a.group + (row0 + r) - i * a.group;
+            float f = 0.0f, f2 = 1.0f;
+            if (ll > 0.0f) {
+                const float de = kNv ? 0.0f : mx - mm, half = rintf(0.5f * de);
+                f = gv / ll * ex2(half);
+                f2 = ex2(de - half);
+            }
+            TQ *dst = static_cast<TQ *>(a.out) + at * D + d;
+            const float y[4] = {v.x * f * f2, v.y * f * f2, v.z * f * f2, v.w * f * f2};
+            if constexpr (sizeof(TQ) == 2) {
+                uint2 w2;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w2.x) : "f"(y[1]), "f"(y[0]));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w2.y) : "f"(y[3]), "f"(y[2]));
+                *reinterpret_cast<uint2 *>(dst) = w2;
+            } else {
+                *reinterpret_cast<float4 *>(dst) = make_float4(y[0], y[1], y[2], y[3]);
+            }
+            if (a.lse && d == 0)
+                a.lse[at] = ll > 0.0f ? (mm + (log2f(ll) - kAttnBias)) * kLn2 : -INFINITY;
+        } else {
+            const int64_t base = ((int64_t)blockIdx.x * R + r);
+            *reinterpret_cast<float4 *>(a.partial + base * D + d) = v;
+            if (d == 0)
+                a.stats[base] = make_float4(mm, ll, mx, 0.0f);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The splits' results, merged: one warp per query row, splits in order.
+// ---------------------------------------------------------------------------
+template <typename TQ, bool kNv, int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads) kv_attention_merge_kernel(const AttnArgs a)
+{
+    constexpr int R = 8 * NT, E = D / 32;
+    pdl_begin();
+    const int lane = (int)threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * kAttnWarps + (threadIdx.x >> 5);
+    if (row >= (int64_t)a.batch * a.c.heads * a.rows)
+        return;
+    const int bh = (int)(row / a.rows), r = (int)(row - (int64_t)bh * a.rows);
+    const int b = bh / a.c.heads, kvh = bh - b * a.c.heads, rt = r / R, row0 = rt * R;
+    const int rows = min(R, a.rows - row0);
+    const AttnSpan sp = attn_span(a, b, row0 / a.group, (row0 + rows - 1) / a.group);
+    if (sp.ns <= 1)
+        return; // written whole
+    const int64_t base = ((int64_t)bh * a.row_tiles + rt) * a.splits;
+    float mm = -INFINITY, mx = -INFINITY;
+    for (int s = lane; s < sp.ns; s += 32) {
+        const float4 st = __ldcg(a.stats + (base + s) * R + (r - row0));
+        mm = fmaxf(mm, st.x);
+        mx = fmaxf(mx, st.z);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, d));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+    }
+    float v[E], ll = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        v[e] = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < sp.ns; ++s) {
+        const float4 st = __ldcg(a.stats + (base + s) * R + (r - row0));
+        const float *p = a.partial + ((base + s) * R + (r - row0)) * D;
+        const float fl = st.y > 0.0f ? ex2(st.x - mm) : 0.0f, f = st.y > 0.0f ? ex2(st.z - mx) : 0.0f;
+        ll = fmaf(st.y, fl, ll);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            v[e] = fmaf(__ldcg(p + e * 32 + lane), f, v[e]);
+    }
+    const int i = r / a.group;
+    const int64_t at = ((int64_t)b * a.q_tokens + i) * a.q_heads + kvh * a.group + r - i * a.group;
+    const float gv = kNv ? __ldcg(a.c.g[1] + kvh) : 1.0f;
+    float f = 0.0f, f2 = 1.0f;
+    if (ll > 0.0f) {
+        const float de = kNv ? 0.0f : mx - mm, half = rintf(0.5f * de);
+        f = gv / ll * ex2(half);
+        f2 = ex2(de - half);
+    }
+    TQ *dst = static_cast<TQ *>(a.out) + at * D;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        dst[e * 32 + lane] = to_out<TQ>(v[e] * f * f2);
     if (a.lse && lane == 0)
-        a.lse[row] = l > 0.0f ? m + logf(l) : -INFINITY;
+        a.lse[at] = ll > 0.0f ? (mm + (log2f(ll) - kAttnBias)) * kLn2 : -INFINITY;
 }
 
 } // namespace fp4

@@ -7,9 +7,17 @@
 
 #include <cstdint>
 
-#include "fp4_attention.cuh"
+#include "fp4_kernels.cuh"
 
 namespace fp4 {
+
+template <typename T> __device__ __forceinline__ float to_f32(T v)
+{
+    if constexpr (sizeof(T) == 2)
+        return __uint_as_float((uint32_t)v << 16);
+    else
+        return v;
+}
 
 // Byte of the MMA scale layout that holds the scale of (row, block).
 __device__ __forceinline__ int64_t mma_scale_at(int64_t row, int64_t block, int64_t tiles_per_band)

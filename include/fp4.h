@@ -537,8 +537,9 @@ fp4_status fp4_kv_read(const fp4_kv_cache *cache, const int64_t *slots, int64_t 
  * is rounded off.
  * Written for few new tokens: the cache is read once for every 16 rows of
  * q_tokens * q_heads / heads (8 for head_dim 256 or fp32 q); a long prompt reads it back with fp4_kv_read for
- * a dense attention.  One kernel; the workspace must be zero-filled once
- * before its first use, and every call leaves its counters at zero. */
+ * a dense attention.  One kernel, and a second one where the tokens are
+ * split over CTAs; the workspace (any contents) holds the splits' results,
+ * and its size depends on head_dim alone. */
 size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache *cache, int64_t batch, int64_t q_tokens, int64_t q_heads,
                                         int64_t table_width);
 fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const void *q, fp4_dtype dtype, int64_t batch,

@@ -153,7 +153,7 @@ def check_attention(c, q, table, lens, scale, window, got=None):
     out, lse = got if got is not None else fp4.kv_attention(q, c, table, torch.tensor(lens, dtype=torch.int32).cuda(), scale=scale, window=window)
     c.check()
     k, v = sequences(c, table, lens)
-    o, s, tol, ltol = ref.attention(q, k, v, lens, scale, window)
+    o, s, tol, ltol = ref.attention(q, k, v, lens, scale, window, c.fmt == MX)
     tol = tol + ref.HALF[q.dtype] * np.abs(o) + 1e-30
     err = np.abs(out.double().cpu().numpy() - o)
     assert (err <= tol).all(), (np.max(err / tol), np.unravel_index(np.argmax(err / tol), err.shape))
