@@ -83,7 +83,7 @@ fp4_status launch_attention_t(const fp4::AttnArgs &a, int64_t blocks, cudaStream
         return st;
     const int64_t lines = (int64_t)a.batch * a.c.heads * a.rows;
     return launch_cfg(fp4::kv_attention_merge_kernel<TQ, kNv, D, NT>,
-                      dim3((unsigned)((lines + fp4::kAttnWarps - 1) / fp4::kAttnWarps)), fp4::kAttnThreads, 0, stream, a);
+                      dim3((unsigned)lines), fp4::kAttnThreads, 0, stream, a);
 }
 
 template <typename TQ, bool kNv>

@@ -26,9 +26,10 @@
 //            movmatrix.
 // Query rows enter as fp16 after a power of two that brings the row's maximum
 // to 2^14 (exact for bf16 but for elements 2^-38 below the maximum); fp32
-// rows as two fp16 terms.  Softmax weights enter as fp16 scaled by 2^15, so
-// that weights down to 2^-29 of the largest keep all their bits and the rest
-// down to 2^-39 some; fp32 calls add a second term.
+// rows as two fp16 terms.  Softmax weights enter as fp16 scaled by 2^11 over
+// a reference that the running maximum passes by at most 2^4, so that weights
+// down to 2^-25 of the largest keep all their bits and the rest down to 2^-36
+// some; fp32 calls add a second term.
 //
 // MXFP4: a block scale 2^e does not fit fp16.  Inside a token the scales are
 // taken relative to the token's largest, 2^(e - E) (0 below 2^-24); 2^E of a
@@ -72,8 +73,15 @@ struct AttnArgs {
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnStep = 32;       // tokens of a warp's step
-constexpr float kAttnBias = 15.0f;  // weights enter the tensor cores times 2^15
+// Weights enter the tensor cores times 2^kAttnBias, and pass the reference
+// by at most 2^kAttnSlack: 2^15 is the largest power of two in fp16.
+constexpr float kAttnBias = 11.0f, kAttnSlack = 4.0f;
+constexpr float kAttnNone = 1e30f;  // minus this: the reference before the first score
 constexpr float kLn2 = 0.693147180559945309f;
+
+// CTAs that share an SM.
+template <typename TQ, int D, int NT>
+constexpr int kAttnCtas = sizeof(TQ) == 4 ? (D == 256 ? 2 : D == 128 ? 3 : 4) : D == 256 ? 3 : D == 64 ? (NT == 2 ? 4 : 5) : (NT == 2 ? 3 : 4);
 
 template <int D> constexpr int kAttnStages = D == 64 ? 4 : D == 128 ? 3 : 2;
 
@@ -143,6 +151,21 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v)
     return r;
 }
 
+// The eight codes of a word as f16 pairs (byte j of the word in h[j]).
+__device__ __forceinline__ void e2m1_word(uint32_t w, uint32_t (&h)[4])
+{
+    asm("{\n\t"
+        ".reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t"
+        "}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
 // 2^-d as f16 bits, d >= 0: normal to d = 14, subnormal to 24, then 0.
 __device__ __forceinline__ uint32_t f16_exp2_neg(int d)
 {
@@ -178,11 +201,39 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int b, int firs
     return s;
 }
 
+// What turns a row's summed output into its result: g / l, and for MXFP4
+// 2^(m' - m), in two factors because the power alone may leave fp32's range.
+// (Sums and weights both carry 2^kAttnBias.)
+struct AttnScale {
+    float f, f2;
+};
+
+template <bool kNv>
+__device__ __forceinline__ AttnScale attn_scale(const AttnArgs &a, int kvh, float m, float mw, float l)
+{
+    AttnScale s = {0.0f, 1.0f};
+    if (l > 0.0f) {
+        if constexpr (kNv) {
+            s.f = __ldcg(a.c.g[1] + kvh) / l;
+        } else {
+            const float half = rintf(0.5f * (mw - m));
+            s.f = ex2(half) / l;
+            s.f2 = ex2((mw - m) - half);
+        }
+    }
+    return s;
+}
+
+__device__ __forceinline__ float attn_lse(float m, float l)
+{
+    return l > 0.0f ? (m + (log2f(l) - kAttnBias)) * kLn2 : -INFINITY;
+}
+
 // ---------------------------------------------------------------------------
 // TQ: uint16_t (bf16) or float.
 // ---------------------------------------------------------------------------
 template <typename TQ, bool kNv, int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attention_kernel(const AttnArgs a)
 {
     constexpr int kParts = sizeof(TQ) == 4 ? 2 : 1; // fp16 terms of a query element and of a weight
     constexpr int G = kNv ? 16 : 32, NB = D / G;    // scale bytes of a token
@@ -191,7 +242,6 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
     constexpr int KS = D / 16; // k steps of the scores = 16-element tiles of the output
     constexpr int R = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(16) uint16_t s_q[kParts][R][D + 8];
     __shared__ float s_exp[R]; // 2^(exponent taken out of the row)
 
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -215,9 +265,9 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
     const int page16 = a.c.page >> 4;
     const int64_t pages = a.c.slots / a.c.page;
 
-    // 16-token granule `gr` (in 16-token units of the sequence): its page
-    // table entry, -1 when no token of it is needed.
-    auto entry = [&](int gr) -> int {
+    // Row (in tokens of this head) of the cache that holds the 16-token
+    // granule `gr` of the sequence, -1 when no token of it is needed.
+    auto granule_row = [&](int gr) -> int64_t {
         if (gr * 16 >= end)
             return -1;
         const int pi = page16 == 1 ? gr : (int)__umul64hi((uint64_t)(uint32_t)gr, a.page_magic);
@@ -226,65 +276,84 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
             raise_status(a.status, kStatusIndex);
             return -1;
         }
-        return e;
-    };
-    // Row (16 tokens of this head) of a granule, in units of tokens.
-    auto granule_row = [&](int gr, int e) -> int64_t {
-        const int pi = page16 == 1 ? gr : (int)__umul64hi((uint64_t)(uint32_t)gr, a.page_magic);
         return ((int64_t)e * a.c.heads + kvh) * a.c.page + (int64_t)(gr - pi * page16) * 16;
+    };
+    // Each lane looks up one granule of the warp's next 16 steps (lane 2 s + h:
+    // granule h of step s); a step's copies take theirs by shuffle.
+    constexpr int kGrStep = 2 * kAttnWarps; // granules between a warp's steps
+    const int gr0 = (tok0 >> 4) + 2 * warp;
+    auto look_up = [&](int s16) -> int64_t {
+        return granule_row(gr0 + (s16 * 16 + (lane >> 1)) * kGrStep + (lane & 1));
     };
     // Copies of one step into a stage.  Chunks of 16 bytes: codes D / 32 per
     // token, swizzled so that both operands' reads are free of bank
-    // conflicts; scales NB per granule.
-    auto issue = [&](int s, int e0, int e1) {
-        uint8_t *st = ring + (s % kStages) * kStage;
-        const uint32_t dst = smem_addr(st);
-        const int gr = (tok0 + kAttnStep * (warp + kAttnWarps * s)) >> 4;
+    // conflicts; scale bytes of the 32 keys, then of the 32 values.  A step
+    // inside one page is contiguous in each array (every page of a multiple
+    // of 32 tokens without a window); otherwise its two granules go apart.
+    constexpr int kPer = D / 32; // chunks of a token
+    const uint8_t *const kp = a.c.packed[0] + lane * 16, *const vp = a.c.packed[1] + lane * 16;
+    // swizzles, the same for every 8 tokens on: XORed into the chunk's index
+    const uint32_t lane_tok = (uint32_t)lane / kPer;
+    const uint32_t kdst = (uint32_t)lane ^ (D == 256 ? lane_tok & 1 : 0u);
+    const uint32_t vdst = (uint32_t)lane ^ (D == 64 ? (lane_tok >> 2 & 1) * 2 : (lane_tok >> 1 & 3) * 2);
+    int64_t ahead = look_up(0);
+    auto copy_codes = [&](uint32_t dst, int64_t row, int first, int count) { // pieces of 32 chunks
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int e = h ? e1 : e0;
-            if (e < 0)
+        for (int i = 0; i < kPer; ++i) {
+            if (i < first || i >= first + count)
                 continue;
-            const int64_t row = granule_row(gr + h, e);
-            constexpr int kPer = D / 32; // chunks of a token
+            // 32 chunks are 32 / kPer tokens: 4 for D = 256, whose swizzle alternates with the piece
+            const uint32_t flip = D == 256 ? (uint32_t)(i & 1) * 4 : 0u;
+            cp_async16(dst + (kdst + 32 * i) * 16, kp + row * (D / 2) + (i - first) * 512);
+            cp_async16(dst + kCodes + ((vdst ^ flip) + 32 * i) * 16, vp + row * (D / 2) + (i - first) * 512);
+        }
+    };
+    auto issue = [&](int s, uint32_t dst) {
+        if (s > 0 && (s & 15) == 0)
+            ahead = look_up(s >> 4);
+        const int64_t row0 = __shfl_sync(0xFFFFFFFFu, ahead, 2 * (s & 15));
+        const int64_t row1 = __shfl_sync(0xFFFFFFFFu, ahead, 2 * (s & 15) + 1);
+        if (row0 >= 0 && row1 == row0 + 16) {
+            copy_codes(dst, row0, 0, kPer);
 #pragma unroll
-            for (int i = 0; i < kPer / 2; ++i) { // 16 tokens: 16 kPer chunks
-                const int c = lane + 32 * i, tk = c / kPer, ch = c % kPer, r = h * 16 + tk;
-                const int64_t src = row * (D / 2) + c * 16;
-                const uint32_t kc = D == 256 ? (uint32_t)(r * kPer + (ch ^ (r & 1))) : (uint32_t)(r * kPer + ch);
-                uint32_t vc;
-                if constexpr (D == 64)
-                    vc = (uint32_t)(r * kPer + ch) ^ (((uint32_t)r >> 2 & 1) * 2);
-                else
-                    vc = (uint32_t)(r * kPer + ch) ^ (((uint32_t)r >> 1 & 3) * 2);
-                cp_async16(dst + kc * 16, a.c.packed[0] + src);
-                cp_async16(dst + kCodes + vc * 16, a.c.packed[1] + src);
+            for (int i = 0; i < 4 * NB; i += 32)
+                if (4 * NB % 32 == 0 || i + lane < 4 * NB) {
+                    const int c = i + lane; // 2 NB chunks of the keys', then of the values'
+                    const uint8_t *src = c < 2 * NB ? a.c.scales[0] + c * 16 : a.c.scales[1] + (c - 2 * NB) * 16;
+                    cp_async16(dst + 2 * kCodes + c * 16, src + row0 * NB);
+                }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t row = h ? row1 : row0;
+                if (row < 0)
+                    continue;
+                copy_codes(dst, row, h * (kPer / 2), kPer / 2);
+                if (lane < 2 * NB) {
+                    const int c = lane < NB ? lane : lane - NB, v = lane >= NB;
+                    cp_async16(dst + 2 * kCodes + v * kScales + h * 16 * NB + c * 16, a.c.scales[v] + row * NB + c * 16);
+                }
             }
-            // lanes below 2 NB: NB chunks of the keys' scales, then of the values'
-            const uint32_t sdst = dst + 2 * kCodes + h * 16 * NB;
-            if (lane < NB)
-                cp_async16(sdst + lane * 16, a.c.scales[0] + row * NB + lane * 16);
-            else if (lane < 2 * NB)
-                cp_async16(sdst + kScales + (lane - NB) * 16, a.c.scales[1] + row * NB + (lane - NB) * 16);
         }
     };
 
+    const uint32_t ring_at = smem_addr(ring);
     // fill the ring before anything else: the copies run under the query's preparation
-    const int gr0 = (tok0 >> 4) + 2 * warp;
-    constexpr int kGrStep = 2 * kAttnWarps; // granules between a warp's steps
-    int e0 = -1, e1 = -1;
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) {
         if (s < steps)
-            issue(s, entry(gr0 + s * kGrStep), entry(gr0 + s * kGrStep + 1));
+            issue(s, ring_at + s * kStage);
         cp_async_commit();
     }
-    if (kStages - 1 < steps) {
-        e0 = entry(gr0 + (kStages - 1) * kGrStep);
-        e1 = entry(gr0 + (kStages - 1) * kGrStep + 1);
-    }
 
-    // Query rows to fp16: a warp takes rows warp, warp + 4, ...
+    // Query rows to fp16: a warp takes rows warp, warp + 4, ..., and stages
+    // them in the last stage of its ring, which the copies above left free.
+    constexpr int kQRow = D + 8;
+    static_assert(kParts * 2 * NT * kQRow * 2 <= kStage, "the staged query rows");
+    auto q_at = [&](int p, int r) -> uint16_t * {
+        uint8_t *const st = smem + ((r % kAttnWarps) * kStages + kStages - 1) * kStage;
+        return reinterpret_cast<uint16_t *>(st) + (p * (R / kAttnWarps) + r / kAttnWarps) * kQRow;
+    };
     for (int r = warp; r < R; r += kAttnWarps) {
         float v[D / 32];
         uint32_t top = 0;
@@ -313,11 +382,11 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
         for (int e = 0; e < D / 32; ++e) {
             const float x = v[e] * up;
             const uint32_t hi = pack_f16x2(x, 0.0f) & 0xFFFFu;
-            s_q[0][r][e * 32 + lane] = (uint16_t)hi;
+            q_at(0, r)[e * 32 + lane] = (uint16_t)hi;
             if constexpr (kParts == 2) {
                 float back, none;
                 f16x2_to_f32(hi, back, none);
-                s_q[1][r][e * 32 + lane] = (uint16_t)(pack_f16x2((x - back) * 2048.0f, 0.0f) & 0xFFFFu);
+                q_at(1, r)[e * 32 + lane] = (uint16_t)(pack_f16x2((x - back) * 2048.0f, 0.0f) & 0xFFFFu);
             }
         }
         if (lane == 0)
@@ -335,7 +404,7 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
         for (int p = 0; p < kParts; ++p)
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(&s_q[p][n * 8 + g][t * (D / 4) + 4 * s]);
+                const uint2 w = *reinterpret_cast<const uint2 *>(q_at(p, n * 8 + g) + t * (D / 4) + 4 * s);
                 qb[p][n][s][0] = w.x;
                 qb[p][n][s][1] = w.y;
             }
@@ -358,27 +427,38 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
                 o[n][i][e] = 0.0f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            m[n][e] = mw[n][e] = -INFINITY;
+            m[n][e] = mw[n][e] = -kAttnNone;
             l[n][e] = 0.0f;
         }
     }
+
+    __syncthreads(); // the staged rows are read: their stages may be filled
 
     // every row of the tile sees all of [all_lo, all_hi]
     const int all_lo = a.window > 0 ? max(0, sp.n - a.q_tokens + (row0 + rows - 1) / a.group - (int)min(a.window, (int64_t)0x40000000) + 1) : 0;
     const int all_hi = sp.n - a.q_tokens + i0;
 
+    uint32_t v_at[2]; // the lane's codes of the values of tokens 2t and 2t + 1
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t r = (uint32_t)(2 * t + c);
+        if constexpr (D == 64)
+            v_at[c] = ((r * 2 + (g >> 2)) ^ ((r >> 2 & 1) * 2)) * 16 + (g & 3) * 4;
+        else if constexpr (D == 128)
+            v_at[c] = ((r * 4 + (g >> 1)) ^ ((r >> 1 & 3) * 2)) * 16 + (g & 1) * 8;
+        else
+            v_at[c] = ((r * 8 + g) ^ ((r >> 1 & 3) * 2)) * 16;
+    }
+    uint32_t rd = 0, wr = (kStages - 1) * kStage; // the stage to read, and the one to fill
     for (int s = 0; s < steps; ++s) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
         if (s + kStages - 1 < steps)
-            issue(s + kStages - 1, e0, e1);
+            issue(s + kStages - 1, ring_at + wr);
         cp_async_commit();
-        e0 = e1 = -1;
-        if (s + kStages < steps) {
-            e0 = entry(gr0 + (s + kStages) * kGrStep);
-            e1 = entry(gr0 + (s + kStages) * kGrStep + 1);
-        }
-        uint8_t *const st = ring + (s % kStages) * kStage;
+        uint8_t *const st = ring + rd;
+        wr = rd;
+        rd = rd == (kStages - 1) * kStage ? 0 : rd + kStage;
         uint8_t *const ks = st + 2 * kCodes, *const vs = ks + kScales;
         const int tok = tok0 + kAttnStep * (warp + kAttnWarps * s);
         const bool edge = tok < all_lo || tok + kAttnStep - 1 > all_hi;
@@ -462,18 +542,23 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
                 }
             }
 #pragma unroll
-            for (int k = 0; k < KS; ++k) { // word k / 2, its half k % 2: elements 4 k .. 4 k + 3
-                uint32_t f[2][2];
+            for (int wd = 0; wd < W; ++wd) { // two k steps a word: elements 8 wd .. 8 wd + 7
+                uint32_t f[2][4];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 2; ++u) {
+                    e2m1_word(w[u][wd], f[u]);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        f[u][j] = f16x2_mul(e2m1x2_to_f16x2(w[u][k / 2] >> (16 * (k & 1) + 8 * j)), sc[u][k / 4]);
+                    for (int j = 0; j < 4; ++j)
+                        f[u][j] = f16x2_mul(f[u][j], sc[u][wd / 2]);
+                }
 #pragma unroll
-                for (int p = 0; p < kParts; ++p)
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma_f16(acc[p][n], f[0][0], f[1][0], f[0][1], f[1][1], qb[p][n][k][0], qb[p][n][k][1]);
+                    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16(acc[p][n], f[0][2 * k], f[1][2 * k], f[0][2 * k + 1], f[1][2 * k + 1],
+                                    qb[p][n][2 * wd + k][0], qb[p][n][2 * wd + k][1]);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -519,46 +604,52 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
                     ev[mt][u] = (float)((int)top - 127);
                 }
         }
-        bool changed = false;
-        float alpha[NT][2], ref[NT][2];
+        // The reference of a row's weights follows its maximum only when a
+        // score passes it by more than kAttnSlack: most steps then need no
+        // exchange between lanes and no rescaling.
+        bool passed = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float top = fmaxf(fmaxf(x[n][0][e], x[n][0][e + 2]), fmaxf(x[n][1][e], x[n][1][e + 2]));
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                const float mn = fmaxf(m[n][e], top);
-                if constexpr (kNv) {
-                    changed |= mn > mw[n][e];
-                    alpha[n][e] = mn > mw[n][e] ? ex2(mw[n][e] - mn) : 1.0f;
-                    l[n][e] *= alpha[n][e];
-                    mw[n][e] = mn;
-                } else {
-                    if (mn > m[n][e])
-                        l[n][e] *= ex2(m[n][e] - mn);
-                    float tw = fmaxf(fmaxf(x[n][0][e] + ev[0][0], x[n][0][e + 2] + ev[0][1]),
-                                     fmaxf(x[n][1][e] + ev[1][0], x[n][1][e + 2] + ev[1][1]));
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1)
-                        tw = fmaxf(tw, __shfl_xor_sync(0xFFFFFFFFu, tw, d));
-                    const float mwn = fmaxf(mw[n][e], tw);
-                    changed |= mwn > mw[n][e];
-                    alpha[n][e] = mwn > mw[n][e] ? ex2(mw[n][e] - mwn) : 1.0f;
-                    mw[n][e] = mwn;
+                const float top = fmaxf(fmaxf(x[n][0][e], x[n][0][e + 2]), fmaxf(x[n][1][e], x[n][1][e + 2]));
+                passed |= top > m[n][e] + kAttnSlack;
+                if constexpr (!kNv) {
+                    const float tw = fmaxf(fmaxf(x[n][0][e] + ev[0][0], x[n][0][e + 2] + ev[0][1]),
+                                           fmaxf(x[n][1][e] + ev[1][0], x[n][1][e + 2] + ev[1][1]));
+                    passed |= tw > mw[n][e] + kAttnSlack;
                 }
-                m[n][e] = mn;
-                ref[n][e] = mn == -INFINITY ? 0.0f : mn; // a row that has seen nothing yet
             }
-        if (__any_sync(0xFFFFFFFFu, changed)) {
+        if (__any_sync(0xFFFFFFFFu, passed)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < KS; ++i)
+                for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(fmaxf(x[n][0][e], x[n][0][e + 2]), fmaxf(x[n][1][e], x[n][1][e + 2]));
+                    float tw = top;
+                    if constexpr (!kNv)
+                        tw = fmaxf(fmaxf(x[n][0][e] + ev[0][0], x[n][0][e + 2] + ev[0][1]),
+                                   fmaxf(x[n][1][e] + ev[1][0], x[n][1][e + 2] + ev[1][1]));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[n][i][e] *= alpha[n][e & 1];
+                    for (int d = 4; d < 32; d <<= 1) {
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                        if constexpr (!kNv)
+                            tw = fmaxf(tw, __shfl_xor_sync(0xFFFFFFFFu, tw, d));
+                    }
+                    if constexpr (kNv)
+                        tw = top;
+                    // (a row that has seen nothing yet has the reference -kAttnNone, below any score)
+                    const float mn = fmaxf(m[n][e], top), mwn = fmaxf(mw[n][e], tw);
+                    l[n][e] *= ex2(m[n][e] - mn);
+                    const float alpha = ex2(mw[n][e] - mwn);
+                    m[n][e] = mn;
+                    mw[n][e] = mwn;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        o[n][i][e] *= alpha;
+                        o[n][i][e + 2] *= alpha;
+                    }
+                }
         }
         // weights of rows 2t, 2t + 1 for token g of each 8: transposed, they are the operand of row g
         uint32_t pb[kParts][NT][2][2];
@@ -573,11 +664,11 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
                     for (int e = 0; e < 2; ++e) {
                         const float xx = x[n][mt][2 * u + e];
                         if constexpr (kNv) {
-                            p[e] = ex2(xx - (ref[n][e] - kAttnBias));
+                            p[e] = ex2(xx - (m[n][e] - kAttnBias));
                             l[n][e] += p[e];
                         } else {
-                            l[n][e] += ex2(xx - (ref[n][e] - kAttnBias));
-                            p[e] = ex2(xx + ev[mt][u] - ((mw[n][e] == -INFINITY ? 0.0f : mw[n][e]) - kAttnBias));
+                            l[n][e] += ex2(xx - (m[n][e] - kAttnBias));
+                            p[e] = ex2(xx + ev[mt][u] - (mw[n][e] - kAttnBias));
                         }
                     }
                     const uint32_t hi = pack_f16x2(p[0], p[1]);
@@ -596,19 +687,15 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
             uint32_t w[4][W];                      // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const uint32_t r = (uint32_t)(mt * 16 + 2 * t + (c & 1) + (c >> 1) * 8);
-                const uint8_t *v = st + kCodes;
+                const uint8_t *v = st + kCodes + v_at[c & 1] + (mt * 16 + (c >> 1) * 8) * (D / 2);
                 if constexpr (D == 64) {
-                    const uint32_t ch = (r * 2 + (g >> 2)) ^ ((r >> 2 & 1) * 2);
-                    w[c][0] = *reinterpret_cast<const uint32_t *>(v + ch * 16 + (g & 3) * 4);
+                    w[c][0] = *reinterpret_cast<const uint32_t *>(v);
                 } else if constexpr (D == 128) {
-                    const uint32_t ch = (r * 4 + (g >> 1)) ^ ((r >> 1 & 3) * 2);
-                    const uint2 x2 = *reinterpret_cast<const uint2 *>(v + ch * 16 + (g & 1) * 8);
+                    const uint2 x2 = *reinterpret_cast<const uint2 *>(v);
                     w[c][0] = x2.x;
                     w[c][1] = x2.y;
                 } else {
-                    const uint32_t ch = (r * 8 + g) ^ ((r >> 1 & 3) * 2);
-                    const uint4 x4 = *reinterpret_cast<const uint4 *>(v + ch * 16);
+                    const uint4 x4 = *reinterpret_cast<const uint4 *>(v);
                     w[c][0] = x4.x;
                     w[c][1] = x4.y;
                     w[c][2] = x4.z;
@@ -651,31 +738,46 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
                 }
             }
             // the lane's D / 8 elements: its first D / 16 are the low rows of
-            // the output tiles, its last D / 16 the high ones
+            // the output tiles, its last D / 16 the high ones.  D >= 128: a
+            // word of the first half with the same word of the second; D = 64:
+            // the one word is both halves.
 #pragma unroll
-            for (int j = 0; j < D / 16; j += 2) { // elements j, j + 1 of each half
-                uint32_t f[2][2][2]; // [half][token pair][element]
+            for (int wd = 0; wd < (W + 1) / 2; ++wd) {
+                uint32_t ev_[2][2][4], od_[2][2][4]; // [half][token pair][byte]: even and odd elements of the pairs
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int el = h * (D / 16) + j, word = el / 8, byte = (el % 8) / 2;
+                for (int h = 0; h < (W > 1 ? 2 : 1); ++h)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const uint32_t w0 = w[2 * c][word], w1 = w[2 * c + 1][word];
-                        // byte: (token's element, next token's element)
-                        const uint32_t ev_ = (w0 & 0x0F0F0F0Fu) | ((w1 & 0x0F0F0F0Fu) << 4);
-                        const uint32_t od_ = ((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u);
-                        f[h][c][0] = f16x2_mul(e2m1x2_to_f16x2(ev_ >> (8 * byte)), sv[c][el / 16 % SB]);
-                        f[h][c][1] = f16x2_mul(e2m1x2_to_f16x2(od_ >> (8 * byte)), sv[c][el / 16 % SB]);
+                        const uint32_t w0 = w[2 * c][h * (W / 2) + wd], w1 = w[2 * c + 1][h * (W / 2) + wd];
+                        // a byte: (token's element, next token's element)
+                        e2m1_word((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), ev_[h][c]);
+                        e2m1_word(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), od_[h][c]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            ev_[h][c][j] = f16x2_mul(ev_[h][c][j], sv[c][h % SB]);
+                            od_[h][c][j] = f16x2_mul(od_[h][c][j], sv[c][h % SB]);
+                        }
                     }
-                }
+                // element 2 j (+ 1) of a half: byte j; D = 64: bytes 0, 1 are the first half, 2, 3 the second
+                constexpr int kBytes = W > 1 ? 4 : 2;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int j = 0; j < kBytes; ++j)
 #pragma unroll
-                    for (int p = 0; p < kParts; ++p)
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t fa[4];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma_f16(o[n][j + i], f[0][0][i], f[1][0][i], f[0][1][i], f[1][1][i], pb[p][n][mt][0],
-                                    pb[p][n][mt][1]);
+                        for (int c = 0; c < 2; ++c) {
+                            const int h1 = W > 1 ? 1 : 0, j1 = W > 1 ? j : j + 2;
+                            fa[2 * c] = i ? od_[0][c][j] : ev_[0][c][j];
+                            fa[2 * c + 1] = i ? od_[h1][c][j1] : ev_[h1][c][j1];
+                        }
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16(o[n][wd * 8 + 2 * j + i], fa[0], fa[1], fa[2], fa[3], pb[p][n][mt][0],
+                                        pb[p][n][mt][1]);
+                    }
             }
         }
     }
@@ -704,11 +806,10 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
             }
         }
     __syncthreads();
-    const float gv = kNv ? __ldcg(a.c.g[1] + kvh) : 1.0f;
     const bool whole = sp.ns <= 1;
     for (int idx = (int)threadIdx.x; idx < rows * (D / 4); idx += kAttnThreads) {
         const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
-        float mm = -INFINITY, mx = -INFINITY, ll = 0.0f;
+        float mm = -kAttnNone, mx = -kAttnNone, ll = 0.0f;
 #pragma unroll
         for (int w = 0; w < kAttnWarps; ++w) {
             mm = fmaxf(mm, s_stats[w][r].x);
@@ -729,17 +830,11 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
             }
         }
         if (whole) {
-            // sums and weights both carry 2^bias; the values 2^(m' - m)
             const int i = (row0 + r) / a.group;
             const int64_t at = ((int64_t)b * a.q_tokens + i) * a.q_heads + kvh * a.group + (row0 + r) - i * a.group;
-            float f = 0.0f, f2 = 1.0f;
-            if (ll > 0.0f) {
-                const float de = kNv ? 0.0f : mx - mm, half = rintf(0.5f * de);
-                f = gv / ll * ex2(half);
-                f2 = ex2(de - half);
-            }
+            const AttnScale f = attn_scale<kNv>(a, kvh, mm, mx, ll);
             TQ *dst = static_cast<TQ *>(a.out) + at * D + d;
-            const float y[4] = {v.x * f * f2, v.y * f * f2, v.z * f * f2, v.w * f * f2};
+            const float y[4] = {v.x * f.f * f.f2, v.y * f.f * f.f2, v.z * f.f * f.f2, v.w * f.f * f.f2};
             if constexpr (sizeof(TQ) == 2) {
                 uint2 w2;
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w2.x) : "f"(y[1]), "f"(y[0]));
@@ -749,7 +844,7 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
                 *reinterpret_cast<float4 *>(dst) = make_float4(y[0], y[1], y[2], y[3]);
             }
             if (a.lse && d == 0)
-                a.lse[at] = ll > 0.0f ? (mm + (log2f(ll) - kAttnBias)) * kLn2 : -INFINITY;
+                a.lse[at] = attn_lse(mm, ll);
         } else {
             const int64_t base = ((int64_t)blockIdx.x * R + r);
             *reinterpret_cast<float4 *>(a.partial + base * D + d) = v;
@@ -760,27 +855,29 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const AttnAr
 }
 
 // ---------------------------------------------------------------------------
-// The splits' results, merged: one warp per query row, splits in order.
+// The splits' results, merged: one CTA per query row.  Its warps take every
+// fourth split, a lane D / 32 neighbouring elements, and meet in shared
+// memory, always in the same order.
 // ---------------------------------------------------------------------------
 template <typename TQ, bool kNv, int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads) kv_attention_merge_kernel(const AttnArgs a)
 {
     constexpr int R = 8 * NT, E = D / 32;
+    __shared__ float s_top[2][kAttnWarps], s_sum[kAttnWarps], s_v[kAttnWarps][D];
     pdl_begin();
-    const int lane = (int)threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kAttnWarps + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.batch * a.c.heads * a.rows)
-        return;
-    const int bh = (int)(row / a.rows), r = (int)(row - (int64_t)bh * a.rows);
+    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+    const int bh = (int)blockIdx.x / a.rows, r = (int)blockIdx.x - bh * a.rows;
     const int b = bh / a.c.heads, kvh = bh - b * a.c.heads, rt = r / R, row0 = rt * R;
     const int rows = min(R, a.rows - row0);
     const AttnSpan sp = attn_span(a, b, row0 / a.group, (row0 + rows - 1) / a.group);
     if (sp.ns <= 1)
         return; // written whole
     const int64_t base = ((int64_t)bh * a.row_tiles + rt) * a.splits;
-    float mm = -INFINITY, mx = -INFINITY;
-    for (int s = lane; s < sp.ns; s += 32) {
-        const float4 st = __ldcg(a.stats + (base + s) * R + (r - row0));
+    const float4 *const stats = a.stats + base * R + (r - row0);
+    const float *const part = a.partial + (base * R + (r - row0)) * D + lane * E;
+    float mm = -kAttnNone, mx = -kAttnNone;
+    for (int s = (int)threadIdx.x; s < sp.ns; s += kAttnThreads) {
+        const float4 st = __ldcg(stats + (int64_t)s * R);
         mm = fmaxf(mm, st.x);
         mx = fmaxf(mx, st.z);
     }
@@ -789,35 +886,68 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_merge_kernel(const 
         mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, d));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
     }
+    if (lane == 0) {
+        s_top[0][warp] = mm;
+        s_top[1][warp] = mx;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+        mm = fmaxf(mm, s_top[0][w]);
+        mx = fmaxf(mx, s_top[1][w]);
+    }
     float v[E], ll = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e)
         v[e] = 0.0f;
-#pragma unroll 4
-    for (int s = 0; s < sp.ns; ++s) {
-        const float4 st = __ldcg(a.stats + (base + s) * R + (r - row0));
-        const float *p = a.partial + ((base + s) * R + (r - row0)) * D;
-        const float fl = st.y > 0.0f ? ex2(st.x - mm) : 0.0f, f = st.y > 0.0f ? ex2(st.z - mx) : 0.0f;
-        ll = fmaf(st.y, fl, ll);
+#pragma unroll 8
+    for (int s = warp; s < sp.ns; s += kAttnWarps) {
+        const float4 st = __ldcg(stats + (int64_t)s * R);
+        const float *p = part + (int64_t)s * R * D;
+        float w[E];
+        if constexpr (E == 2) {
+            const float2 p2 = __ldcg(reinterpret_cast<const float2 *>(p));
+            w[0] = p2.x;
+            w[1] = p2.y;
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+                const float4 p4 = __ldcg(reinterpret_cast<const float4 *>(p + e));
+                w[e] = p4.x;
+                w[e + 1] = p4.y;
+                w[e + 2] = p4.z;
+                w[e + 3] = p4.w;
+            }
+        }
+        const float f = ex2(st.z - mx);
+        ll = fmaf(st.y, ex2(st.x - mm), ll);
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            v[e] = fmaf(__ldcg(p + e * 32 + lane), f, v[e]);
+            v[e] = fmaf(w[e], f, v[e]);
     }
-    const int i = r / a.group;
-    const int64_t at = ((int64_t)b * a.q_tokens + i) * a.q_heads + kvh * a.group + r - i * a.group;
-    const float gv = kNv ? __ldcg(a.c.g[1] + kvh) : 1.0f;
-    float f = 0.0f, f2 = 1.0f;
-    if (ll > 0.0f) {
-        const float de = kNv ? 0.0f : mx - mm, half = rintf(0.5f * de);
-        f = gv / ll * ex2(half);
-        f2 = ex2(de - half);
-    }
-    TQ *dst = static_cast<TQ *>(a.out) + at * D;
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        dst[e * 32 + lane] = to_out<TQ>(v[e] * f * f2);
-    if (a.lse && lane == 0)
-        a.lse[at] = ll > 0.0f ? (mm + (log2f(ll) - kAttnBias)) * kLn2 : -INFINITY;
+        s_v[warp][lane * E + e] = v[e];
+    if (lane == 0)
+        s_sum[warp] = ll;
+    __syncthreads();
+    ll = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w)
+        ll += s_sum[w];
+    const int i = r / a.group;
+    const int64_t at = ((int64_t)b * a.q_tokens + i) * a.q_heads + kvh * a.group + r - i * a.group;
+    const AttnScale f = attn_scale<kNv>(a, kvh, mm, mx, ll);
+    TQ *dst = static_cast<TQ *>(a.out) + at * D;
+    for (int d = (int)threadIdx.x; d < D; d += kAttnThreads) {
+        float y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w)
+            y += s_v[w][d];
+        dst[d] = to_out<TQ>(y * f.f * f.f2);
+    }
+    if (a.lse && threadIdx.x == 0)
+        a.lse[at] = attn_lse(mm, ll);
 }
 
 } // namespace fp4

@@ -11,12 +11,13 @@ in) and are evaluated element by element next to the exact value:
   softmax   an error dx of a score changes its weight by the factor e^dx, the
             quotient of two such sums by 2 dx; a weight rounded to fp16 is off
             by 2^-11 (two terms: 2^-21); exponential and logarithm by 2^-20.
-            Weights are held times 2^15 in fp16, whose spacing ends at 2^-24:
-            below 2^-14 a weight is off by up to half of that, 2^-25, which is
-            2^-40 of the largest weight (one), whatever the weight's own size,
-            so a result by 2^-40 sum_j |v_j|.  MXFP4 holds w_j 2^(E_j) relative
+            Weights are held times 2^11 (over a reference at most the largest
+            weight) in fp16, whose spacing ends at 2^-24: below 2^-14 a weight
+            is off by up to half of that, 2^-25, which is 2^-36 of the largest
+            weight (one), whatever the weight's own size, so a result by 2^-36
+            sum_j |v_j|.  MXFP4 holds w_j 2^(E_j) relative
             to the largest such product (E_j the token's largest block
-            exponent, |v_j| <= 6 2^(E_j)): 2^-40 max_j(w_j 2^(E_j)) sum_j
+            exponent, |v_j| <= 6 2^(E_j)): 2^-36 max_j(w_j 2^(E_j)) sum_j
             |v_j| 2^(-E_j).  With 2^(E_j) <= max_d |v_j| * 2 (the largest
             block holds a code of at least one half wherever it is not zero)
             this is computed from the values themselves.
@@ -99,9 +100,9 @@ def attention(q, k, v, lens, scale, window, mx=False):
                 if mx:
                     big = 2 * np.abs(vv).max(1)
                     unit = np.abs(vv) / np.where(big > 0, big, 1)[:, None] * 12
-                    tol[b, i, h] += 2.0 ** -40 * (w * big).max() * unit.sum(0)
+                    tol[b, i, h] += 2.0 ** -36 * (w * big).max() * unit.sum(0)
                 else:
-                    tol[b, i, h] += 2.0 ** -40 * w.max() * np.abs(vv).sum(0)
+                    tol[b, i, h] += 2.0 ** -36 * w.max() * np.abs(vv).sum(0)
                 ltol[b, i, h] = dx + 2.0 ** -22 * abs(lse[b, i, h]) + ((p - lo + 1) / 16 + 8) * 2.0 ** -23 + 2.0 ** -20
     return out, lse, tol, ltol
 
