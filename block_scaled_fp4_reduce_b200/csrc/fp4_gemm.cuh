@@ -54,21 +54,6 @@
 namespace fp4 {
 
 // ---------------------------------------------------------------------------
-// TMA tile loads (the mbarrier helpers and the bounded wait are in
-// fp4_async.cuh).
-// ---------------------------------------------------------------------------
-// 2-D TMA tile load of box (x = column, y = row) into shared memory,
-// completing on `bar`.  x (the innermost coordinate) times the element size
-// is a multiple of 16 bytes.
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
-                 : "memory");
-}
-
-// ---------------------------------------------------------------------------
 // Scale layout for the MMA, as a tiled transpose.  CTA (band, chunk) takes
 // the 128 rows of one band and kSfKc consecutive 4-block tiles (64 scale
 // bytes per row): it loads the 128 x 64-byte strip with row-contiguous
