@@ -114,12 +114,6 @@ template <int N> __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// 2^-d as f16 bits, d >= 0: normal to d = 14, subnormal to 24, then 0.
-__device__ __forceinline__ uint32_t f16_exp2_neg(int d)
-{
-    return d <= 14 ? (uint32_t)(15 - d) << 10 : (d <= 24 ? 1u << (24 - d) : 0u);
-}
-
 // Largest of the four bytes of v.
 __device__ __forceinline__ uint32_t max_byte(uint32_t v)
 {

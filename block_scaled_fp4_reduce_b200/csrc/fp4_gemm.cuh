@@ -50,6 +50,7 @@
 
 #include "fp4_async.cuh"
 #include "fp4_kernels.cuh"
+#include "fp4_tmem.cuh"
 
 namespace fp4 {
 
@@ -145,15 +146,6 @@ static_assert(kGemmTile * kGemmHalves + kGemmStages * kGemmSfCols <= kGemmTmemCo
 constexpr uint32_t kGemmIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(kGemmTile / 8) << 17) |
                                 ((uint32_t)(kGemmTile / 16) << 24);
 
-// Shared-memory matrix descriptor, K-major, 128-byte swizzle: rows of 128
-// bytes, 8-row groups 1024 bytes apart (SBO 64 x 16 B), LBO 1, descriptor
-// version 1, layout type 2.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr)
-{
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
-           (2ull << 61);
-}
-
 // Shared-memory descriptor of a 512-byte scale tile for tcgen05.cp (32 rows
 // of 16 bytes, K-major without swizzle: 8-row core matrices of 128 bytes,
 // SBO 8 x 16 B), version 1, layout type 0.
@@ -161,22 +153,6 @@ __device__ __forceinline__ uint64_t smem_desc_sf(uint32_t addr)
 {
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | (8ull << 32) | (1ull << 46);
 }
-
-__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols)
-{
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols)
-{
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 __device__ __forceinline__ void tc_copy_sf(uint32_t taddr, uint64_t sdesc)
 {
@@ -192,13 +168,6 @@ __device__ __forceinline__ void tc_mma_nvfp4(uint32_t d_tmem, uint64_t adesc, ui
                  "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], p;\n\t"
                  "}" ::"r"(d_tmem),
                  "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tc_commit(uint64_t *bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_addr(bar))
                  : "memory");
 }
 

@@ -14,113 +14,111 @@
 namespace {
 
 using namespace fp4_launch;
-using fp4::kThreads;
 
-// 2-D tensor map of the packed weight [N, Kp/2] bytes: boxes of 64 bytes x
-// 128 rows, 64-byte swizzle.
-fp4_status weight_map(const uint8_t *p, int64_t N, int64_t Kp, CUtensorMap *map)
+// 2-D tensor map of a row-major matrix: boxes of `box_cols` elements (64 or 128
+// bytes, the swizzle's span) x `box_rows` rows; zeros outside.
+fp4_status matrix_map(CUtensorMapDataType type, int size, const void *p, int64_t rows, int64_t cols, int box_cols,
+                      int box_rows, CUtensorMapSwizzle swizzle, CUtensorMap *map)
 {
     EncodeTiled enc = encode_tiled();
     if (!enc)
         return FP4_ERR_CUDA;
-    const cuuint64_t dims[2] = {(cuuint64_t)(Kp / 2), (cuuint64_t)N};
-    const cuuint64_t strides[1] = {(cuuint64_t)(Kp / 2)};
-    const cuuint32_t box[2] = {64u, (cuuint32_t)fp4::kLinRows};
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(cols * size)};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(p), dims, strides, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = enc(map, type, 2, const_cast<void *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? FP4_OK : FP4_ERR_CUDA;
 }
 
-// Column groups of 8 in a tile: enough for the rows (each `parts` columns),
-// at most 8.
-int tile_groups(int64_t rows, int parts)
-{
-    int nt = parts;
-    while (nt < 8 && (int64_t)8 * nt < rows * parts)
-        nt *= 2;
-    return nt;
-}
-
-// Workspace of the laid-out activations: their fragments, then a power of
-// two for each column.
+// Workspace: the activations as fp16 rows [tiles * cols][Kpad], then an
+// exponent for each.
 struct Layout {
-    int nt, stages;
-    int64_t tiles; // of activation rows
-    size_t frags, bytes;
+    int cols, chunks; // columns of a tile (activation rows x parts, whole sixteens)
+    int64_t tiles, Kpad;
+    size_t xh, bytes;
 };
 
-Layout layout(int64_t rows, int64_t Kp, int parts)
+Layout layout(int64_t rows, int64_t K, int parts)
 {
     Layout l;
-    l.nt = tile_groups(rows, parts);
-    l.stages = (int)((Kp + fp4::kLinStep - 1) / fp4::kLinStep);
-    l.tiles = (rows * parts + 8 * l.nt - 1) / (8 * l.nt);
-    l.frags = (size_t)l.tiles * l.stages * 2 * l.nt * fp4::kLinFrag;
-    l.bytes = l.frags + (size_t)l.tiles * 8 * l.nt * sizeof(float);
+    const int64_t all = rows * parts, most = fp4::kLinMaxCols;
+    l.tiles = (all + most - 1) / most;
+    if (l.tiles < 1)
+        l.tiles = 1;
+    const int64_t per = (rows + l.tiles - 1) / l.tiles; // rows of a tile, spread evenly
+    l.cols = (int)((per * parts + 15) / 16 * 16);
+    l.chunks = (int)((K + fp4::kLinChunk - 1) / fp4::kLinChunk);
+    l.Kpad = (int64_t)l.chunks * fp4::kLinChunk;
+    l.xh = (size_t)(l.tiles * l.cols * l.Kpad) * 2;
+    l.bytes = l.xh + (size_t)(l.tiles * l.cols) * sizeof(int32_t);
     return l;
 }
 
-// CTAs of a cluster: K is split until the grid fills the GPU twice over, as
-// long as every CTA keeps two stages.
-int pick_splits(int64_t tiles, int stages, int sms)
+// Stages of the ring: two CTAs share an SM up to kLinSharedCols columns (at
+// least four stages each), beyond that one CTA has the SM for itself.
+int pick_stages(int cols)
 {
-    int s = 1;
-    while (s < fp4::kLinMaxSplits && tiles * s < 2 * sms && stages >= 4 * s)
-        s *= 2;
-    return s;
+    const int room = cols <= fp4::kLinSharedCols ? 112 * 1024 : 224 * 1024;
+    const int s = (room - 1024 - fp4::lin_landing_bytes(cols)) / fp4::lin_stage_bytes(cols);
+    return s < fp4::kLinMaxStages ? s : fp4::kLinMaxStages;
 }
 
-template <bool kNv, int kNt>
-fp4_status launch_linear(const CUtensorMap &map, fp4::LinearArgs a, int64_t mtiles, int sms, cudaStream_t stream)
+// CTAs of a cluster.  A CTA's time is its chunks and about kLinFixed more for
+// its start and end; what counts is that times the rounds the grid takes.
+int pick_splits(int64_t tiles, int chunks, int64_t slots)
 {
-    auto kernel = fp4::linear_kernel<kNv, kNt>;
-    constexpr int smem = fp4::kLinSmem<kNv, kNt>;
-    if (!smem_attr(kernel, smem))
+    constexpr int kLinFixed = 6;
+    int best = 1;
+    int64_t cost = INT64_MAX;
+    for (int s = 1; s <= fp4::kLinMaxSplits && s <= chunks; ++s) {
+        const int64_t c = (tiles * s + slots - 1) / slots * ((chunks + s - 1) / s + kLinFixed);
+        if (c < cost) {
+            cost = c;
+            best = s;
+        }
+    }
+    return best;
+}
+
+template <bool kNv>
+fp4_status launch_linear(const CUtensorMap &map_w, const CUtensorMap &map_x, fp4::LinearArgs a, int64_t mtiles,
+                         cudaStream_t stream)
+{
+    auto kernel = fp4::linear_kernel<kNv>;
+    int dev = 0;
+    const int sms = sm_count(dev);
+    if (sms <= 0 || !smem_attr(kernel, 224 * 1024))
         return FP4_ERR_CUDA;
-    const int64_t bands = (a.N + fp4::kLinRows - 1) / fp4::kLinRows;
-    const int splits = pick_splits(bands * mtiles, a.stages, sms);
-    cudaLaunchConfig_t cfg = {};
-    if (bands * mtiles > INT_MAX / splits)
+    const int64_t bands = ((int64_t)a.N + fp4::kLinRows - 1) / fp4::kLinRows;
+    if (bands > 65535 || mtiles > 65535)
         return FP4_ERR_SHAPE;
-    a.splits = splits;
-    a.mtiles = (int)mtiles;
-    cfg.gridDim = dim3((unsigned)(bands * mtiles * splits));
+    a.splits = pick_splits(bands * mtiles, a.chunks, (int64_t)sms * (a.cols <= fp4::kLinSharedCols ? 2 : 1));
+    a.share = a.chunks / a.splits;
+    a.more = a.chunks % a.splits;
+    a.own = (fp4::kLinRows + a.splits - 1) / a.splits;
+    a.own_inv = (65536 + a.own - 1) / a.own;
+    a.stages = pick_stages(a.cols);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.splits, (unsigned)mtiles, (unsigned)bands);
     cfg.blockDim = dim3(fp4::kLinThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = (size_t)a.stages * fp4::lin_stage_bytes(a.cols) + fp4::lin_landing_bytes(a.cols) + 1024;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.x = (unsigned)a.splits;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kernel, map, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, map_w, map_x, a) != cudaSuccess) {
         (void)cudaGetLastError();
         return FP4_ERR_CUDA;
     }
     return FP4_OK;
-}
-
-template <typename T, bool kNv>
-fp4_status run_linear(const T *x, int64_t rows, int64_t K, int64_t x_stride, const CUtensorMap &map, fp4::LinearArgs a,
-                      const Layout &l, int sms, cudaStream_t stream)
-{
-    const int64_t packed_rows = l.tiles * 8 * l.nt / a.parts;
-    fp4_status st = launch(fp4::linear_pack_kernel<T, kNv>, (int)packed_rows, stream, x, (int)rows, (int)K, x_stride,
-                           l.nt, 2 * l.stages, const_cast<uint8_t *>(a.frags), const_cast<float *>(a.xs), a.status);
-    if (st != FP4_OK)
-        return st;
-    switch (l.nt) {
-    case 1: return launch_linear<kNv, 1>(map, a, l.tiles, sms, stream);
-    case 2: return launch_linear<kNv, 2>(map, a, l.tiles, sms, stream);
-    case 4: return launch_linear<kNv, 4>(map, a, l.tiles, sms, stream);
-    default: return launch_linear<kNv, 8>(map, a, l.tiles, sms, stream);
-    }
 }
 
 } // namespace
@@ -145,7 +143,7 @@ fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t ro
         return FP4_ERR_INVALID_ARG;
     const int64_t group = fmt == FP4_NVFP4 ? 16 : 32;
     const int64_t in = dtype == FP4_BF16 ? 2 : 4, on = out_dtype == FP4_BF16 ? 2 : 4;
-    if (rows > INT_MAX || K > INT_MAX - 1024 || N > INT_MAX - 1024)
+    if (rows >= (1 << 23) || K > INT_MAX - 1024 || N >= (1 << 23))
         return FP4_ERR_SHAPE;
     const int64_t Kp = (K + group - 1) / group * group;
     if (Kp % 32)
@@ -174,38 +172,44 @@ fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t ro
         return FP4_ERR_WORKSPACE;
     if (!aligned(workspace, 16))
         return FP4_ERR_ALIGN;
-    int dev = 0;
-    const int sms = sm_count(dev);
-    if (sms <= 0)
-        return FP4_ERR_CUDA;
     const int parts = dtype == FP4_F32 ? 2 : 1;
     const Layout l = layout(rows, K, parts);
-    CUtensorMap map;
-    std::memset(&map, 0, sizeof(map));
-    const fp4_status st = weight_map(packed, N, Kp, &map);
+    uint16_t *const xh = static_cast<uint16_t *>(workspace);
+    int32_t *const xe = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + l.xh);
+    const int per = l.cols / parts;
+    CUtensorMap map_w, map_x;
+    std::memset(&map_w, 0, sizeof(map_w));
+    std::memset(&map_x, 0, sizeof(map_x));
+    fp4_status st = matrix_map(CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, packed, N, Kp / 2, fp4::kLinChunk / 2, fp4::kLinRows,
+                               CU_TENSOR_MAP_SWIZZLE_64B, &map_w);
+    if (st == FP4_OK)
+        st = matrix_map(CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, xh, l.tiles * l.cols, l.Kpad, fp4::kLinChunk / 2, l.cols,
+                        CU_TENSOR_MAP_SWIZZLE_128B, &map_x);
+    if (st != FP4_OK)
+        return st;
+    const int packed_rows = (int)(l.tiles * per), Kpad = (int)l.Kpad;
+    st = dtype == FP4_BF16
+             ? launch(fp4::linear_pack_kernel<uint16_t>, packed_rows, stream, static_cast<const uint16_t *>(x), (int)rows,
+                      (int)K, x_stride, per, Kpad, xh, xe, status)
+             : launch(fp4::linear_pack_kernel<float>, packed_rows, stream, static_cast<const float *>(x), (int)rows,
+                      (int)K, x_stride, per, Kpad, xh, xe, status);
     if (st != FP4_OK)
         return st;
     fp4::LinearArgs a = {};
     a.scales = scales_mma;
-    a.frags = static_cast<uint8_t *>(workspace);
-    a.xs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + l.frags);
+    a.xe = xe;
     a.g = global_scale;
     a.y = y;
     a.rows = (int)rows;
     a.N = (int)N;
     a.parts = parts;
-    a.stages = l.stages;
+    a.cols = l.cols;
+    a.chunks = l.chunks;
     a.tiles = (int)((Kp / group + 3) / 4);
     a.out_bf16 = out_dtype == FP4_BF16;
     a.status = status;
-    const bool bf = dtype == FP4_BF16;
-    const uint16_t *xb = static_cast<const uint16_t *>(x);
-    const float *xf = static_cast<const float *>(x);
-    if (fmt == FP4_NVFP4)
-        return bf ? run_linear<uint16_t, true>(xb, rows, K, x_stride, map, a, l, sms, stream)
-                  : run_linear<float, true>(xf, rows, K, x_stride, map, a, l, sms, stream);
-    return bf ? run_linear<uint16_t, false>(xb, rows, K, x_stride, map, a, l, sms, stream)
-              : run_linear<float, false>(xf, rows, K, x_stride, map, a, l, sms, stream);
+    return fmt == FP4_NVFP4 ? launch_linear<true>(map_w, map_x, a, l.tiles, stream)
+                            : launch_linear<false>(map_w, map_x, a, l.tiles, stream);
 }
 
 } // extern "C"

@@ -1,33 +1,36 @@
 // fp4_linear.cuh -- y = x W^^T for a few rows of unquantised activations and
 // an FP4 weight.
 //
-// Bound by reading the weight once (0.53 to 0.56 bytes an element), so the
-// weight is the M operand of the tensor cores: mma.sync m16n8k16 takes 16
-// weight rows and 8 activation rows, the codes become fp16 in registers on
-// their way from shared memory, and one decoded fragment serves every
-// activation row.
+// Bound by reading the weight once (0.53 to 0.56 bytes an element).  The
+// weight is the M operand of tcgen05.mma kind::f16 (128 weight rows, fp16 by
+// fp16 into fp32), so that its codes are decoded once whatever the number of
+// activation rows, which are the N operand.
 //
-//   linear_pack_kernel  activations -> fp16 after a power of two per row that
-//                       brings its maximum to 2^14 (bf16 x: exact but for
-//                       what lies 2^-38 below the maximum; fp32 x: two terms,
-//                       22 bits), written in the order in which the MMA's B
-//                       fragments are read
-//   linear_kernel       a cluster of `splits` CTAs per 128 weight rows and 8
-//                       kNt activation rows; each CTA takes a share of K in
-//                       stages of 256 elements through a ring filled by TMA,
-//                       the partial results meet over distributed shared
-//                       memory, summed in the order of the CTAs
+//   linear_pack_kernel  activations -> fp16 rows after a power of two per row
+//                       that brings the row's maximum to 2^14 (bf16 x: exact
+//                       but for what lies 2^-38 below the maximum; fp32 x: two
+//                       terms, 22 bits, in two rows)
+//   linear_kernel       a cluster of `splits` CTAs per 128 weight rows and up
+//                       to 256 columns (activation rows, or terms of them);
+//                       each CTA takes a share of K in chunks of 128 elements
+//                       through a ring filled by TMA; each row's partial sums
+//                       are written to the CTA of the cluster that owns the
+//                       row (distributed shared memory) and added there in the
+//                       order of the CTAs
 //
-// Fragments (lane = 4 g + t): per 128 elements of K ("chunk"), lane (g, t)
-// reads 32 codes of weight rows g and g + 8.  Which element is which k index
-// of the MMA is free as long as both operands agree:
-//   NVFP4  elements 32 t .. 32 t + 31, one 16-byte load, two blocks of 16; a
-//          code times its E4M3 scale is exact in fp16, so the scale is
-//          multiplied in before the MMA
-//   MXFP4  elements 8 t .. 8 t + 7 of each of the four blocks of 32, so that
-//          two MMAs cover one block: their sum is added in fp32 times one
-//          factor, 2^e and the power of two of the activation row, so that
-//          neither takes the sum out of fp32's range on its own
+// Roles of a CTA: warps 0-3 and 4-7 are two groups of decoders that take
+// chunks in turn.  A decoder thread is one weight row: it reads the row's 64
+// bytes of codes, turns them into fp16 pairs, multiplies the block scales in
+// and stores the row into tensor memory (tcgen05.st; lane = row, two elements
+// a column), where the MMA takes its A operand from: the decoded weight never
+// passes through shared memory.  Warp 8 issues the copies, warp 9 the MMAs.
+// While the MMA reads one decoded chunk the groups write the next ones.
+//
+// Scales: an E2M1 code times an E4M3 scale is exact in fp16.  An E8M0 scale
+// does not fit fp16: MXFP4 weights are decoded relative to the largest scale
+// of their row in the CTA's share of K (found by a scan of the scale bytes
+// before the first chunk), 2^(e - E), which is exact down to 2^-23; the row's
+// 2^E multiplies the sum.
 #pragma once
 
 #include <cstdint>
@@ -37,31 +40,34 @@
 #include "fp4_async.cuh"
 #include "fp4_kernels.cuh"
 #include "fp4_mma.cuh"
+#include "fp4_tmem.cuh"
 
 namespace fp4 {
 
-constexpr int kLinRows = 128;               // weight rows of a CTA
-constexpr int kLinStep = 256;               // elements of K per stage: two chunks of 128
-constexpr int kLinWarps = 8;                // 4 groups of 32 rows x the stage's 2 chunks
-constexpr int kLinThreads = 32 * (kLinWarps + 1); // + the producer
-constexpr int kLinCodes = kLinRows * kLinStep / 2; // 16 KB: two boxes of 64 bytes x 128 rows
-constexpr int kLinFrag = 2048;              // one chunk of 8 activation rows in fragment order
+constexpr int kLinRows = 128;          // weight rows of a CTA
+constexpr int kLinChunk = 128;         // elements of K per stage
+constexpr int kLinDecoders = 8;        // warps
+constexpr int kLinThreads = 32 * (kLinDecoders + 2);
+constexpr int kLinCodes = kLinRows * kLinChunk / 2; // 8 KB
+constexpr int kLinScales = 1024;       // two 512-byte scale tiles (NVFP4; MXFP4 has one)
+constexpr int kLinMaxCols = 256;
+constexpr int kLinMaxStages = 8;
 constexpr int kLinMaxSplits = 8;
 
-template <bool kNv> constexpr int kLinScales = kNv ? 2048 : 1024; // scale tiles of a stage
-template <bool kNv, int kNt> constexpr int kLinStage = kLinCodes + kLinScales<kNv> + 2 * kNt * kLinFrag;
-// Two CTAs share an SM up to 16 activation rows (or terms of them), so that
-// one's start and end run under the other's stream; beyond, the ring of one.
-template <bool kNv, int kNt> constexpr int kLinStages = kNt <= 2 ? 4 : kNt == 4 ? 3 : 4;
-template <bool kNv, int kNt> constexpr int kLinSmem = kLinStages<kNv, kNt> * kLinStage<kNv, kNt> + 1024;
-
-// Address of the 16-byte unit `u` (8 elements) of a chunk of activation row g
-// inside the chunk's 2 KB: [j][lane][8 halves].
-template <bool kNv> __device__ __forceinline__ int lin_frag_at(int g, int u)
+// Partial sums of the rows that a CTA owns, from every CTA of the cluster: in
+// memory of their own up to 32 columns, beyond that in the ring, which then
+// costs a barrier more (every CTA has to be done with its ring).
+constexpr int kLinLandingCols = 32;
+__host__ __device__ constexpr int lin_landing_bytes(int cols)
 {
-    const int t = kNv ? u >> 2 : u & 3, j = kNv ? u & 3 : u >> 2;
-    return j * 512 + (4 * g + t) * 16;
+    return cols <= kLinLandingCols ? cols * 4 * (kLinRows + kLinMaxSplits) : 0;
 }
+__host__ __device__ constexpr int lin_stage_bytes(int cols) { return kLinCodes + kLinScales + cols * kLinChunk * 2; }
+// Tensor memory: the accumulator, then three decoded chunks of 64 columns (two
+// beyond 64 columns, where the CTA has an SM's 512 columns for itself anyway).
+constexpr int kLinSharedCols = 64; // the largest tile with two CTAs on an SM
+__host__ __device__ constexpr int lin_tmem_cols(int cols) { return cols <= kLinSharedCols ? 256 : 512; }
+constexpr int kLinBuffers = 3;
 
 template <typename T> __device__ __forceinline__ float to_f32(T v)
 {
@@ -72,21 +78,22 @@ template <typename T> __device__ __forceinline__ float to_f32(T v)
 }
 
 // ---------------------------------------------------------------------------
-// One CTA per activation row (rows past the last: zeros).  frags: [tile][chunk]
-// [column group of 8][2 KB], fp32 rows as two terms, the second in the
-// groups kNt / 2 on; xs: [tile][8 kNt] the power of two each column stands for.
+// One CTA per activation row, padding rows of the last tile among them (zeros).
+// xh: fp16 [tiles * cols][Kpad]; a tile holds `per` rows and, for fp32 x,
+// their second terms in the rows `per` on.  xe [tiles * cols]: the exponent of
+// the power of two that each of them is to be multiplied by.
 // ---------------------------------------------------------------------------
-template <typename T, bool kNv>
+template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    linear_pack_kernel(const T *__restrict__ x, int rows, int K, int64_t x_stride, int nt, int chunks, uint8_t *frags,
-                       float *xs, int32_t *status)
+    linear_pack_kernel(const T *__restrict__ x, int rows, int K, int64_t x_stride, int per, int Kpad, uint16_t *xh,
+                       int32_t *xe, int32_t *status)
 {
     pdl_begin();
     // the product may start: it waits for this grid before it reads what is written here
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
-    const int row = (int)blockIdx.x;
-    const int per = 8 * nt / kParts, tile = row / per, r = row - tile * per; // rows of a tile
+    const int row = (int)blockIdx.x, tile = row / per;
+    const int64_t to = (int64_t)tile * per * kParts + (row - tile * per);
     const T *src = x + (int64_t)row * x_stride;
     const int n = row < rows ? K : 0;
     const bool vec = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
@@ -113,13 +120,10 @@ __global__ void __launch_bounds__(kThreads)
     // 2^ex <= max < 2^(ex + 1); a row below 2^-112 counts as if its maximum were that
     const int ex = bad ? 14 : max((int)(top >> 23), 15) - 127;
     const float up = __uint_as_float((uint32_t)(127 + (14 - ex)) << 23);
-    const int groups = nt / kParts;
     if (threadIdx.x < kParts)
-        xs[tile * 8 * nt + threadIdx.x * groups * 8 + r] =
-            __uint_as_float((uint32_t)(127 + (ex - 14)) << 23) * (threadIdx.x ? 0x1p-11f : 1.0f);
-    uint8_t *dst = frags + ((int64_t)tile * chunks * nt + (r >> 3)) * kLinFrag;
-    for (int u = (int)threadIdx.x; u < chunks * 16; u += kThreads) { // units of 8 elements
-        const int k = u * 8;
+        xe[to + (threadIdx.x ? per : 0)] = ex - 14 - (threadIdx.x ? 11 : 0);
+    uint16_t *const dst = xh + to * Kpad, *const dst2 = dst + (int64_t)per * Kpad;
+    for (int k = (int)threadIdx.x * 8; k < Kpad; k += kThreads * 8) {
         float v[8];
         if (vec && k + 8 <= n) {
             if constexpr (sizeof(T) == 2) {
@@ -156,287 +160,337 @@ __global__ void __launch_bounds__(kThreads)
                 lo[j] = pack_f16x2((a - ah) * 2048.0f, (b - bh) * 2048.0f);
             }
         }
-        uint8_t *p = dst + (int64_t)(u >> 4) * nt * kLinFrag + lin_frag_at<kNv>(r & 7, u & 15);
-        *reinterpret_cast<uint4 *>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(dst + k) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         if constexpr (kParts == 2)
-            *reinterpret_cast<uint4 *>(p + groups * kLinFrag) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4 *>(dst2 + k) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
 }
 
-__device__ __forceinline__ void cluster_sync()
+// 2^k, -149 <= k <= 127; beyond, 0 and infinity.
+__device__ __forceinline__ float exp2_int(int k)
+{
+    if (k < -126)
+        return k < -149 ? 0.0f : __uint_as_float(1u << (k + 149));
+    return k > 127 ? INFINITY : __uint_as_float((uint32_t)(k + 127) << 23);
+}
+
+__device__ __forceinline__ void cluster_arrive()
 {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 struct LinearArgs {
     const uint8_t *scales; // MMA layout, `tiles` 512-byte tiles per 128-row band
-    const uint8_t *frags;
-    const float *xs, *g;
+    const int32_t *xe;
+    const float *g;
     void *y;
-    int rows, N, parts, stages, tiles, out_bf16;
-    int splits, mtiles; // CTAs of a cluster, tiles of activation rows
+    int rows, N, parts, cols; // cols: columns of a tile
+    int chunks, tiles, stages;
+    int splits;       // CTAs of a cluster (grid x); grid y: tiles of columns, z: bands of the weight
+    int share, more;  // chunks of a CTA, one more for the first `more`
+    int own, own_inv; // weight rows that a CTA owns, and 2^16 / own rounded up
+    int out_bf16;
     int32_t *status;
 };
 
-template <bool kNv, int kNt>
-__global__ void __launch_bounds__(kLinThreads, kNt <= 4 ? 2 : 1)
-    linear_kernel(const __grid_constant__ CUtensorMap map, const LinearArgs a)
+template <bool kNv>
+__global__ void __launch_bounds__(kLinThreads, 2)
+    linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                  const LinearArgs a)
 {
-    constexpr int kStages = kLinStages<kNv, kNt>, kStage = kLinStage<kNv, kNt>;
-    constexpr int kTiles = kLinScales<kNv> / 512; // scale tiles of a stage
-    constexpr int kCols = 8 * kNt;
+    constexpr int kTiles = kNv ? 2 : 1; // scale tiles of a chunk
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
+    __shared__ __align__(8) uint64_t full[kLinMaxStages], empty[kLinMaxStages], ready[kLinBuffers], done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ float2 s_factor[kLinMaxCols]; // the column's power of two, in two factors
+    __shared__ float s_g;
+    __shared__ int consumed; // chunks whose copies the MMA warp has seen land
     uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int unit = (int)blockIdx.x / a.splits, split = (int)blockIdx.x - unit * a.splits; // a cluster a unit
-    const int band = unit / a.mtiles, mtile = unit - band * a.mtiles, splits = a.splits;
-    const int s0 = (int)((int64_t)a.stages * split / splits), s1 = (int)((int64_t)a.stages * (split + 1) / splits);
-    const int n_st = s1 - s0;
+    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+    const int splits = a.splits, split = (int)blockIdx.x, mtile = (int)blockIdx.y, band = (int)blockIdx.z;
+    const int c0 = split * a.share + min(split, a.more), n = a.share + (split < a.more ? 1 : 0);
+    const int stages = a.stages, stage_bytes = lin_stage_bytes(a.cols);
+    const uint32_t tmem_cols = (uint32_t)lin_tmem_cols(a.cols);
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+    // Copies.  The weight is no work of the packing grid's, which runs only
+    // once everything before it is done: the first stages of it are asked for
+    // before that grid ends, the activations after.
+    auto weight = [&](int i, int s) {
+        const int c = c0 + i;
+        uint8_t *const st = smem + s * stage_bytes;
+        const uint32_t scale_bytes = (uint32_t)min(kTiles, a.tiles - c * kTiles) * 512u;
+        mbar_expect_tx(&full[s], (uint32_t)(kLinCodes + a.cols * kLinChunk * 2) + scale_bytes);
+        tma_load_2d(st, &map_w, c * (kLinChunk / 2), band * kLinRows, &full[s]);
+        bulk_load(st + kLinCodes, a.scales + ((int64_t)band * a.tiles + (int64_t)c * kTiles) * 512, scale_bytes, &full[s]);
+    };
+    auto activations = [&](int i, int s) {
+        const int c = c0 + i;
+        uint8_t *const st = smem + s * stage_bytes + kLinCodes + kLinScales;
+        tma_load_2d(st, &map_x, c * kLinChunk, mtile * a.cols, &full[s]);
+        tma_load_2d(st + a.cols * kLinChunk, &map_x, c * kLinChunk + kLinChunk / 2, mtile * a.cols, &full[s]);
+    };
+    const int first = n < stages ? n : stages;
+    const int groups = a.cols / a.parts, have = min(groups, a.rows - mtile * groups); // activation rows of the tile
+    cluster_arrive(); // this CTA runs: the others may write to its shared memory
+    if (warp == kLinDecoders && elect_one()) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kLinWarps);
+            mbar_init(&empty[s], 1);
         }
+        for (int i = 0; i < kLinBuffers; ++i)
+            mbar_init(&ready[i], kLinDecoders / 2);
+        mbar_init(&done, 1);
         mbar_init_fence();
+        consumed = 0;
+        weight(0, 0); // the others once the rest of the CTA may go on
     }
-    // Scale bytes past the last tile are never copied: they must not be NaN.
-    for (int i = (int)threadIdx.x; i < kStages * kLinScales<kNv> / 16; i += kLinThreads) {
-        const int s = i / (kLinScales<kNv> / 16), at = i - s * (kLinScales<kNv> / 16);
-        *reinterpret_cast<uint4 *>(smem + s * kStage + kLinCodes + at * 16) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (warp == kLinDecoders + 1)
+        tmem_alloc(&tmem_slot, tmem_cols);
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot, tmem_a = tmem + (uint32_t)a.cols;
 
-    float acc[2][kNt][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int n = 0; n < kNt; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[i][n][e] = 0.0f;
     bool timed_out = false;
-
-    if (warp == kLinWarps) {
-        // Producer.  The weight is no work of the packing grid's, which runs
-        // only once everything before it is done: its stages are asked for
-        // before that grid ends, the activations after.
-        auto weight = [&](int i) {
-            const int s = i % kStages, k = s0 + i;
-            uint8_t *const st = smem + s * kStage;
-            const int tiles = min(kTiles, a.tiles - k * kTiles);
-            mbar_expect_tx(&full[s], (uint32_t)(kLinCodes + tiles * 512 + 2 * kNt * kLinFrag));
-            tma_load_2d(st, &map, k * 128, band * kLinRows, &full[s]);
-            tma_load_2d(st + kLinCodes / 2, &map, k * 128 + 64, band * kLinRows, &full[s]);
-            bulk_load(st + kLinCodes, a.scales + ((int64_t)band * a.tiles + (int64_t)k * kTiles) * 512,
-                      (uint32_t)tiles * 512u, &full[s]);
-        };
-        auto activations = [&](int i) {
-            const int s = i % kStages, k = s0 + i;
-            bulk_load(smem + s * kStage + kLinCodes + kLinScales<kNv>,
-                      a.frags + ((int64_t)mtile * a.stages + k) * (2 * kNt * kLinFrag), 2 * kNt * kLinFrag, &full[s]);
-        };
-        const int first = n_st < kStages ? n_st : kStages;
-        if (lane == 0)
-            for (int i = 0; i < first; ++i)
-                weight(i);
-        pdl_begin();
-        if (lane == 0)
-            for (int i = 0; i < first; ++i)
-                activations(i);
+    int issued = 0;
+    uint32_t top = 0; // MXFP4: the largest scale byte of the thread's row in this share
+    if (warp == kLinDecoders) {
+        // (positions in the ring are carried along: a division by the run-time
+        // number of stages costs more than the rest of a step)
+        if (elect_one())
+            for (int i = 1; i < first; ++i)
+                weight(i, i);
         __syncwarp();
-        int issued = first;
-        for (int i = first; i < n_st; ++i) {
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[i % kStages], (uint32_t)(i / kStages - 1) & 1u))) {
+        pdl_begin();
+        if (elect_one())
+            for (int i = 0; i < first; ++i)
+                activations(i, i);
+        __syncwarp();
+        issued = first;
+        uint32_t phase = 0;
+        for (int i = first, s = 0; i < n; ++i) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], phase))) {
                 timed_out = true;
                 break;
             }
-            if (lane == 0) {
-                weight(i);
-                activations(i);
+            if (elect_one()) {
+                weight(i, s);
+                activations(i, s);
             }
             __syncwarp();
             ++issued;
-        }
-        // the last copies land before the shared memory has another use
-        for (int i = issued - kStages > 0 ? issued - kStages : 0; i < issued; ++i)
-            if (!mbar_wait(&full[i % kStages], (uint32_t)(i / kStages) & 1u))
-                timed_out = true;
-    } else {
-        pdl_begin();
-        const int wr = warp & 3, wk = warp >> 2; // rows 32 wr .. + 31, chunk wk of every stage
-        float xs[kNt][2];
-        if constexpr (!kNv) {
-#pragma unroll
-            for (int n = 0; n < kNt; ++n) {
-                const float2 v = __ldcg(reinterpret_cast<const float2 *>(a.xs + mtile * kCols + n * 8 + 2 * t));
-                xs[n][0] = v.x;
-                xs[n][1] = v.y;
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1u;
             }
         }
-        for (int i = 0; i < n_st; ++i) {
-            const int s = i % kStages;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (uint32_t)(i / kStages) & 1u))) {
+    } else if (warp == kLinDecoders + 1) {
+        // MMAs: eight of K = 16 per chunk, A from tensor memory.  elect.sync, not
+        // a test of the lane: the compiler then knows that one thread issues and
+        // keeps the descriptors in uniform registers (measured alone at N = 16:
+        // 10 cycles per MMA against 46).
+        pdl_begin();
+        for (int i = lane; i < a.cols; i += 32) { // for the epilogue
+            const int e = __ldcg(a.xe + mtile * a.cols + i), e2 = e >> 1;
+            s_factor[i] = make_float2(exp2_int(e2), exp2_int(e - e2));
+        }
+        if (kNv && lane == 0)
+            s_g = __ldcg(a.g);
+        const uint32_t idesc = (1u << 4) | ((uint32_t)(a.cols / 8) << 17) | ((uint32_t)(kLinRows / 16) << 24);
+        const uint64_t x0 = smem_desc_sw128(smem_addr(smem + kLinCodes + kLinScales));
+        const uint32_t half = (uint32_t)a.cols * kLinChunk / 16, step = (uint32_t)stage_bytes / 16; // in descriptor units
+        uint32_t phase = 0, ready_phase = 0;
+        for (int i = 0, s = 0, b = 0; i < n; ++i) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[s], phase))) {
                 timed_out = true;
                 break;
             }
-            const uint8_t *const st = smem + s * kStage;
-            const uint8_t *const codes = st + wk * (kLinCodes / 2);
-            const uint8_t *const sf = st + kLinCodes + wk * (kLinScales<kNv> / 2);
-            const uint4 *const xf = reinterpret_cast<const uint4 *>(st + kLinCodes + kLinScales<kNv> + wk * kNt * kLinFrag) + lane;
-            // row r of the band: codes at 64 r (16-byte chunks swizzled by
-            // (r / 2) % 4), scale word at 16 (r % 32) + 4 (r / 32); the warp's
-            // rows are 32 wr + 16 i + 8 u + g
-            if constexpr (kNv) {
-                uint32_t w[2][2][4], sc[2][2][2];
+            if (lane == 0)
+                consumed = i + 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ready[b], ready_phase))) {
+                timed_out = true;
+                break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t x = x0 + (uint64_t)((uint32_t)s * step);
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int r = 16 * m + 8 * u + g;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(codes + (wr * 32 + r) * 64 + ((t ^ (r >> 1 & 3)) * 16));
-                        w[m][u][0] = v.x;
-                        w[m][u][1] = v.y;
-                        w[m][u][2] = v.z;
-                        w[m][u][3] = v.w;
-                        const uint32_t f = e4m3x2_to_f16x2(
-                            *reinterpret_cast<const uint16_t *>(sf + (t >> 1) * 512 + r * 16 + wr * 4 + (t & 1) * 2));
-                        sc[m][u][0] = __byte_perm(f, f, 0x1010);
-                        sc[m][u][1] = __byte_perm(f, f, 0x3232);
-                    }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) { // 8 elements of each lane: two k steps
-                    uint4 b[kNt];
-#pragma unroll
-                    for (int n = 0; n < kNt; ++n)
-                        b[n] = xf[(n * kLinFrag + j * 512) / 16];
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        uint32_t f[2][4];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            e2m1_word(w[m][u][j], f[u]);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                f[u][q] = f16x2_mul(f[u][q], sc[m][u][j >> 1]);
-                        }
-#pragma unroll
-                        for (int n = 0; n < kNt; ++n) {
-                            mma_f16(acc[m][n], f[0][0], f[1][0], f[0][1], f[1][1], b[n].x, b[n].y);
-                            mma_f16(acc[m][n], f[0][2], f[1][2], f[0][3], f[1][3], b[n].z, b[n].w);
-                        }
-                    }
-                }
-            } else {
-                uint32_t se[2][2];
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        se[m][u] = *reinterpret_cast<const uint32_t *>(sf + (16 * m + 8 * u + g) * 16 + wr * 4);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) { // block j of the chunk
-                    uint4 b[kNt];
-#pragma unroll
-                    for (int n = 0; n < kNt; ++n)
-                        b[n] = xf[(n * kLinFrag + j * 512) / 16];
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        uint32_t f[2][4];
-                        float e[2];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int r = 16 * m + 8 * u + g;
-                            e2m1_word(*reinterpret_cast<const uint32_t *>(codes + (wr * 32 + r) * 64 +
-                                                                          ((j ^ (r >> 1 & 3)) * 16) + 4 * t),
-                                      f[u]);
-                            e[u] = e8m0_to_f32((se[m][u] >> (8 * j)) & 0xFFu);
-                        }
-#pragma unroll
-                        for (int n = 0; n < kNt; ++n) {
-                            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma_f16(c, f[0][0], f[1][0], f[0][1], f[1][1], b[n].x, b[n].y);
-                            mma_f16(c, f[0][2], f[1][2], f[0][3], f[1][3], b[n].z, b[n].w);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                acc[m][n][q] = fmaf(c[q], xs[n][q & 1] * e[q >> 1], acc[m][n][q]);
-                        }
-                    }
-                }
+                for (int k = 0; k < 8; ++k)
+                    tc_mma_f16_ts(tmem, tmem_a + (uint32_t)(64 * b + 8 * k),
+                                  x + (uint64_t)((k >> 2) * half + (uint32_t)(k & 3) * 2), idesc, (i | k) != 0);
+                tc_commit(&empty[s]);
             }
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&empty[s]);
-        }
-    }
-    if (timed_out)
-        raise_status(a.status, kStatusTimeout);
-
-    // ---- the two chunk halves, then the CTAs of the cluster ----
-    float *const part = reinterpret_cast<float *>(smem); // [column][128 rows]
-    __syncthreads();
-    const int wr = warp & 3;
-    auto at = [&](int m, int n, int q) { return (n * 8 + 2 * t + (q & 1)) * kLinRows + wr * 32 + 16 * m + 8 * (q >> 1) + g; };
-    if (warp < kLinWarps && warp >= 4) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int n = 0; n < kNt; ++n)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    part[at(m, n, q)] = acc[m][n][q];
-    }
-    __syncthreads();
-    if (warp < 4) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int n = 0; n < kNt; ++n)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    part[at(m, n, q)] += acc[m][n][q];
-    }
-    cluster_sync();
-    const int per = kLinRows / splits, groups = kCols / a.parts; // weight rows of this CTA, activation rows of the tile
-    const float gw = kNv ? __ldcg(a.g) : 1.0f;
-    for (int i = (int)threadIdx.x; i < groups * per; i += kLinThreads) {
-        const int m = i / per, r = split * per + (i - m * per);
-        const int row = mtile * groups + m, col = band * kLinRows + r;
-        if (row >= a.rows || col >= a.N)
-            continue;
-        auto column = [&](int c) { // summed over the cluster, in order
-            const uint32_t src = smem_addr(part + c * kLinRows + r);
-            float v = 0.0f;
-            for (int s = 0; s < splits; ++s) {
-                uint32_t remote;
-                float f;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(src), "r"(s));
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(remote) : "memory");
-                v += f;
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1u;
             }
-            return v;
-        };
-        // (in double: g and the row's power of two may take turns out of fp32's range)
-        double y = column(m);
-        if constexpr (kNv)
-            y *= (double)__ldcg(a.xs + mtile * kCols + m);
-        if (a.parts == 2) {
-            double lo = column(groups + m);
-            if constexpr (kNv)
-                lo *= (double)__ldcg(a.xs + mtile * kCols + groups + m);
-            y += lo;
+            if (++b == kLinBuffers) {
+                b = 0;
+                ready_phase ^= 1u;
+            }
         }
-        const float out = kNv ? (float)(y * (double)gw) : (float)y;
-        const int64_t o = (int64_t)row * a.N + col;
-        if (a.out_bf16)
-            static_cast<uint16_t *>(a.y)[o] = to_out<uint16_t>(out);
-        else
-            static_cast<float *>(a.y)[o] = out;
+        if (elect_one())
+            tc_commit(&done);
+        __syncwarp();
+    } else {
+        const int group = warp >> 2, quarter = warp & 3; // rows 32 quarter .. + 31: the tensor-memory lanes this warp reaches
+        const int row = quarter * 32 + lane, word = lane * 16 + quarter * 4; // its scale word in a tile
+        if constexpr (!kNv) {
+            const uint8_t *p = a.scales + ((int64_t)band * a.tiles + c0) * 512 + word;
+            uint32_t m4 = 0;
+            const int tiles = min(c0 + n, a.tiles) - c0;
+#pragma unroll 8
+            for (int i = 0; i < tiles; ++i)
+                m4 = __vmaxu4(m4, __ldg(reinterpret_cast<const uint32_t *>(p + (int64_t)i * 512)));
+            top = max(max(m4 & 0xFFu, (m4 >> 8) & 0xFFu), max((m4 >> 16) & 0xFFu, m4 >> 24));
+        }
+        // positions of this chunk in the ring and among the buffers, and of the
+        // chunk that the buffer held before
+        int s = group, b = group, old = group;
+        uint32_t phase = 0, old_phase = 0;
+        for (int i = group; i < n; i += 2) {
+            bool ok = mbar_wait(&full[s], phase);
+            if (i >= kLinBuffers) { // the MMA has read what the buffer held, chunk i - 3
+                ok = ok && mbar_wait(&empty[old], old_phase);
+            }
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                timed_out = true;
+                break;
+            }
+            const uint8_t *const st = smem + s * stage_bytes;
+            const uint8_t *const codes = st + row * 64, *const sf = st + kLinCodes + word;
+            const uint32_t dst = tmem_a + (uint32_t)(64 * b) + ((uint32_t)(quarter * 32) << 16);
+            uint32_t s4[kTiles];
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+                // (a weight's last chunk may have one tile alone; nothing is copied past it)
+                s4[j] = j == 0 || (c0 + i) * kTiles + j < a.tiles ? *reinterpret_cast<const uint32_t *>(sf + j * 512) : 0u;
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) { // 64 elements
+                uint32_t f[32];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) { // 32 elements: one 16-byte read
+                    const int ch = 2 * h + q;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(codes + ((ch ^ (row >> 1 & 3)) * 16));
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t sc[2];
+                    if constexpr (kNv) { // blocks 2 ch, 2 ch + 1
+                        const uint32_t p = e4m3x2_to_f16x2(s4[h] >> (16 * q));
+                        sc[0] = __byte_perm(p, p, 0x1010);
+                        sc[1] = __byte_perm(p, p, 0x3232);
+                    } else {
+                        sc[0] = sc[1] = f16_exp2_neg((int)top - (int)((s4[0] >> (8 * ch)) & 0xFFu)) * 0x10001u;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t d[4];
+                        e2m1_word(w[j], d);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            f[16 * q + 4 * j + e] = f16x2_mul(d[e], sc[j >> 1]);
+                    }
+                }
+                tc_store_32(dst + (uint32_t)(32 * h), f);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&ready[b]);
+            if (i >= kLinBuffers)
+                old += 2;
+            else
+                old = i + 2 - kLinBuffers; // chunk 0 or 1: the first that a buffer is taken from
+            if (old >= stages) {
+                old -= stages;
+                old_phase ^= 1u;
+            }
+            s += 2;
+            if (s >= stages) {
+                s -= stages;
+                phase ^= 1u;
+            }
+            b += 2;
+            if (b >= kLinBuffers)
+                b -= kLinBuffers;
+        }
+        pdl_begin(); // what is read and written below follows the packing grid
     }
-    cluster_sync();
+
+    // ---- the sums, times g or 2^E and the column's power of two, to the CTA that owns the row ----
+    const bool ok = mbar_wait(&done, 0);
+    if (!ok || timed_out)
+        raise_status(a.status, kStatusTimeout);
+    if (warp == kLinDecoders) // copies that nobody waited for (only after a timeout) land before the CTA ends
+        for (int i = consumed; i < issued; ++i)
+            (void)mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u);
+    float *const land = reinterpret_cast<float *>(smem + (a.cols <= kLinLandingCols ? stages * stage_bytes : 0)); // [CTA][column][its rows]
+    cluster_wait(); // every CTA of the cluster runs
+    if (a.cols > kLinLandingCols) {
+        cluster_arrive();
+        cluster_wait(); // and is done with its ring
+    }
+    if (warp < kLinDecoders) {
+        tc_fence_after();
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const int owner = (row * a.own_inv) >> 16; // row / own
+        uint32_t to;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(to)
+                     : "r"(smem_addr(land + split * a.cols * a.own + row - owner * a.own)), "r"(owner));
+        // The row's factor (g, or 2^E) between the two halves of the column's:
+        // neither alone need keep a sum inside fp32's range that both together
+        // leave there.
+        const float r = kNv ? s_g : e8m0_to_f32(top);
+        for (int p = 0; p < a.parts; ++p)
+            for (int c = p * groups + (warp >> 2) * 8; c < p * groups + have; c += 16) {
+                float v[8];
+                tc_load_8(tmem + (uint32_t)c + ((uint32_t)(quarter * 32) << 16), v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 f = s_factor[c + j];
+                    const float y = v[j] * f.x * r * f.y;
+                    if (c + j < p * groups + have)
+                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (uint32_t)((c + j) * a.own * 4)), "f"(y)
+                                     : "memory");
+                }
+            }
+    }
+    tc_fence_before();
+    cluster_arrive();
+    cluster_wait();
+    if (warp == kLinDecoders + 1)
+        tmem_dealloc(tmem, tmem_cols);
+
+    // ---- the rows of this CTA, summed over the cluster in order ----
+    const int col0 = band * kLinRows + split * a.own;
+    const int mine = min(min(a.own, kLinRows - split * a.own), a.N - col0);
+    for (int m = warp; m < have; m += kLinThreads / 32)
+        for (int r = lane; r < mine; r += 32) {
+            float y = 0.0f;
+            for (int p = 0; p < a.parts; ++p) {
+                const float *const src = land + (p * groups + m) * a.own + r;
+#pragma unroll
+                for (int s = 0; s < kLinMaxSplits; ++s)
+                    if (s < splits)
+                        y += src[s * a.cols * a.own];
+            }
+            const int64_t o = (int64_t)(mtile * groups + m) * a.N + col0 + r;
+            if (a.out_bf16)
+                static_cast<uint16_t *>(a.y)[o] = to_out<uint16_t>(y);
+            else
+                static_cast<float *>(a.y)[o] = y;
+        }
 }
 
 } // namespace fp4

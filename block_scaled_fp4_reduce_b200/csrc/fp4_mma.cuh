@@ -61,4 +61,10 @@ __device__ __forceinline__ void e2m1_word(uint32_t w, uint32_t (&h)[4])
         : "r"(w));
 }
 
+// 2^-d as f16 bits, d >= 0: normal to d = 14, subnormal to 24, then 0.
+__device__ __forceinline__ uint32_t f16_exp2_neg(int d)
+{
+    return d <= 14 ? (uint32_t)(15 - d) << 10 : (d <= 24 ? 1u << (24 - d) : 0u);
+}
+
 } // namespace fp4

@@ -560,7 +560,8 @@ fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const void *q, fp4_dtype 
  * row (fp32 x as two terms, 22 bits): bf16 x is exact but for what lies
  * below 2^-38 of its row's largest value.  Products are summed in fp32.
  * A NaN or Inf in x sets NONFINITE (its row of y is then unspecified, the
- * others are not).  N, K, rows below 2^31.  rows or N = 0: nothing is done;
+ * others are not).  N and rows
+ * below 2^23, K below 2^31 - 1024 (else FP4_ERR_SHAPE).  rows or N = 0: nothing is done;
  * K = 0: y = 0.  Reads the weight once for every 64 rows (32 for fp32 x).  Two kernels;
  * the workspace (any contents) holds the laid-out activations. */
 size_t fp4_linear_workspace_bytes(int64_t rows, int64_t K);
