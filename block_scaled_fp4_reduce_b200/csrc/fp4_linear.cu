@@ -3,6 +3,7 @@
 #include <climits>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -56,13 +57,19 @@ Layout layout(int64_t rows, int64_t K, int parts)
     return l;
 }
 
-// Stages of the ring: two CTAs share an SM up to kLinSharedCols columns (at
-// least four stages each), beyond that one CTA has the SM for itself.
-int pick_stages(int cols)
+// Stages of the ring: two CTAs share an SM up to kLinSharedCols columns,
+// beyond that one CTA has the SM for itself.  fused: the chunks whose
+// activations lie beside the ring, 0 where they come packed.
+int pick_stages(int cols, int fused, size_t &smem)
 {
     const int room = cols <= fp4::kLinSharedCols ? 112 * 1024 : 224 * 1024;
-    const int s = (room - 1024 - fp4::lin_landing_bytes(cols)) / fp4::lin_stage_bytes(cols);
-    return s < fp4::kLinMaxStages ? s : fp4::kLinMaxStages;
+    const int fixed = 1024 + fp4::lin_landing_bytes(cols) + fused * cols * fp4::kLinChunk * 2;
+    const int stage = fp4::lin_stage_bytes(cols, fused > 0);
+    int s = (room - fixed) / stage;
+    if (s > fp4::kLinMaxStages)
+        s = fp4::kLinMaxStages;
+    smem = (size_t)s * stage + fixed;
+    return s;
 }
 
 // CTAs of a cluster.  A CTA's time is its chunks and about kLinFixed more for
@@ -82,28 +89,22 @@ int pick_splits(int64_t tiles, int chunks, int64_t slots)
     return best;
 }
 
-template <bool kNv>
+template <bool kNv, typename T>
 fp4_status launch_linear(const CUtensorMap &map_w, const CUtensorMap &map_x, fp4::LinearArgs a, int64_t mtiles,
-                         cudaStream_t stream)
+                         int64_t bands, cudaStream_t stream)
 {
-    auto kernel = fp4::linear_kernel<kNv>;
-    int dev = 0;
-    const int sms = sm_count(dev);
-    if (sms <= 0 || !smem_attr(kernel, 224 * 1024))
+    auto kernel = fp4::linear_kernel<kNv, T>;
+    if (!smem_attr(kernel, 224 * 1024))
         return FP4_ERR_CUDA;
-    const int64_t bands = ((int64_t)a.N + fp4::kLinRows - 1) / fp4::kLinRows;
-    if (bands > 65535 || mtiles > 65535)
-        return FP4_ERR_SHAPE;
-    a.splits = pick_splits(bands * mtiles, a.chunks, (int64_t)sms * (a.cols <= fp4::kLinSharedCols ? 2 : 1));
     a.share = a.chunks / a.splits;
     a.more = a.chunks % a.splits;
+    a.most_share = a.share + (a.more > 0);
     a.own = (fp4::kLinRows + a.splits - 1) / a.splits;
     a.own_inv = (65536 + a.own - 1) / a.own;
-    a.stages = pick_stages(a.cols);
     cudaLaunchConfig_t cfg = {};
+    a.stages = pick_stages(a.cols, std::is_void_v<T> ? 0 : a.most_share, cfg.dynamicSmemBytes);
     cfg.gridDim = dim3((unsigned)a.splits, (unsigned)mtiles, (unsigned)bands);
     cfg.blockDim = dim3(fp4::kLinThreads);
-    cfg.dynamicSmemBytes = (size_t)a.stages * fp4::lin_stage_bytes(a.cols) + fp4::lin_landing_bytes(a.cols) + 1024;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -172,32 +173,27 @@ fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t ro
         return FP4_ERR_WORKSPACE;
     if (!aligned(workspace, 16))
         return FP4_ERR_ALIGN;
+    int dev = 0;
+    const int sms = sm_count(dev);
+    if (sms <= 0)
+        return FP4_ERR_CUDA;
     const int parts = dtype == FP4_F32 ? 2 : 1;
     const Layout l = layout(rows, K, parts);
-    uint16_t *const xh = static_cast<uint16_t *>(workspace);
-    int32_t *const xe = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + l.xh);
-    const int per = l.cols / parts;
+    const int64_t bands = (N + fp4::kLinRows - 1) / fp4::kLinRows;
+    if (bands > 65535 || l.tiles > 65535)
+        return FP4_ERR_SHAPE;
     CUtensorMap map_w, map_x;
     std::memset(&map_w, 0, sizeof(map_w));
     std::memset(&map_x, 0, sizeof(map_x));
     fp4_status st = matrix_map(CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, packed, N, Kp / 2, fp4::kLinChunk / 2, fp4::kLinRows,
                                CU_TENSOR_MAP_SWIZZLE_64B, &map_w);
-    if (st == FP4_OK)
-        st = matrix_map(CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, xh, l.tiles * l.cols, l.Kpad, fp4::kLinChunk / 2, l.cols,
-                        CU_TENSOR_MAP_SWIZZLE_128B, &map_x);
-    if (st != FP4_OK)
-        return st;
-    const int packed_rows = (int)(l.tiles * per), Kpad = (int)l.Kpad;
-    st = dtype == FP4_BF16
-             ? launch(fp4::linear_pack_kernel<uint16_t>, packed_rows, stream, static_cast<const uint16_t *>(x), (int)rows,
-                      (int)K, x_stride, per, Kpad, xh, xe, status)
-             : launch(fp4::linear_pack_kernel<float>, packed_rows, stream, static_cast<const float *>(x), (int)rows,
-                      (int)K, x_stride, per, Kpad, xh, xe, status);
     if (st != FP4_OK)
         return st;
     fp4::LinearArgs a = {};
+    a.x = x;
+    a.x_stride = x_stride;
+    a.K = (int)K;
     a.scales = scales_mma;
-    a.xe = xe;
     a.g = global_scale;
     a.y = y;
     a.rows = (int)rows;
@@ -208,8 +204,32 @@ fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t ro
     a.tiles = (int)((Kp / group + 3) / 4);
     a.out_bf16 = out_dtype == FP4_BF16;
     a.status = status;
-    return fmt == FP4_NVFP4 ? launch_linear<true>(map_w, map_x, a, l.tiles, stream)
-                            : launch_linear<false>(map_w, map_x, a, l.tiles, stream);
+    a.splits = pick_splits(bands * l.tiles, a.chunks, (int64_t)sms * (a.cols <= fp4::kLinSharedCols ? 2 : 1));
+    const bool bf = dtype == FP4_BF16, nv = fmt == FP4_NVFP4;
+    const int share = (a.chunks + a.splits - 1) / a.splits;
+    if (a.cols <= fp4::kLinFusedCols && share <= fp4::kLinFusedShare && rows * share <= fp4::kLinFusedWork) {
+        if (nv)
+            return bf ? launch_linear<true, uint16_t>(map_w, map_x, a, l.tiles, bands, stream)
+                      : launch_linear<true, float>(map_w, map_x, a, l.tiles, bands, stream);
+        return bf ? launch_linear<false, uint16_t>(map_w, map_x, a, l.tiles, bands, stream)
+                  : launch_linear<false, float>(map_w, map_x, a, l.tiles, bands, stream);
+    }
+    uint16_t *const xh = static_cast<uint16_t *>(workspace);
+    int32_t *const xe = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + l.xh);
+    a.xe = xe;
+    st = matrix_map(CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, xh, l.tiles * l.cols, l.Kpad, fp4::kLinChunk / 2, l.cols,
+                    CU_TENSOR_MAP_SWIZZLE_128B, &map_x);
+    if (st != FP4_OK)
+        return st;
+    const int per = l.cols / parts, packed_rows = (int)(l.tiles * per), Kpad = (int)l.Kpad;
+    st = bf ? launch(fp4::linear_pack_kernel<uint16_t>, packed_rows, stream, static_cast<const uint16_t *>(x), (int)rows,
+                     (int)K, x_stride, per, Kpad, xh, xe, status)
+            : launch(fp4::linear_pack_kernel<float>, packed_rows, stream, static_cast<const float *>(x), (int)rows, (int)K,
+                     x_stride, per, Kpad, xh, xe, status);
+    if (st != FP4_OK)
+        return st;
+    return nv ? launch_linear<true, void>(map_w, map_x, a, l.tiles, bands, stream)
+              : launch_linear<false, void>(map_w, map_x, a, l.tiles, bands, stream);
 }
 
 } // extern "C"

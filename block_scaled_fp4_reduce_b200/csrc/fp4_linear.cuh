@@ -34,6 +34,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -62,7 +63,17 @@ __host__ __device__ constexpr int lin_landing_bytes(int cols)
 {
     return cols <= kLinLandingCols ? cols * 4 * (kLinRows + kLinMaxSplits) : 0;
 }
-__host__ __device__ constexpr int lin_stage_bytes(int cols) { return kLinCodes + kLinScales + cols * kLinChunk * 2; }
+// Where a CTA's share of the activations is small, the decoders lay it out
+// themselves, in shared memory, while the first codes are on their way: no
+// packing grid and no workspace.  The most columns, chunks of K, and rows x
+// chunks (beyond that the layout takes longer than the packing grid).
+constexpr int kLinFusedCols = 16, kLinFusedShare = 16, kLinFusedWork = 32;
+
+// Codes and scales of a chunk, with its activations where those come packed.
+__host__ __device__ constexpr int lin_stage_bytes(int cols, bool fused)
+{
+    return kLinCodes + kLinScales + (fused ? 0 : cols * kLinChunk * 2);
+}
 // Tensor memory: the accumulator, then three decoded chunks of 64 columns (two
 // beyond 64 columns, where the CTA has an SM's 512 columns for itself anyway).
 constexpr int kLinSharedCols = 64; // the largest tile with two CTAs on an SM
@@ -75,6 +86,59 @@ template <typename T> __device__ __forceinline__ float to_f32(T v)
         return __uint_as_float((uint32_t)v << 16);
     else
         return v;
+}
+
+// fp16 terms of eight activations times `up`.
+template <int kParts>
+__device__ __forceinline__ void lin_terms(const float (&v)[8], float up, uint32_t (&hi)[4], uint32_t (&lo)[4])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float a = v[2 * j] * up, b = v[2 * j + 1] * up;
+        hi[j] = pack_f16x2(a, b);
+        if constexpr (kParts == 2) {
+            float ah, bh;
+            f16x2_to_f32(hi[j], ah, bh);
+            lo[j] = pack_f16x2((a - ah) * 2048.0f, (b - bh) * 2048.0f);
+        }
+    }
+}
+
+// Eight activations from k on, zeros from n on; vec: 16-byte aligned.
+template <typename T> __device__ __forceinline__ void lin_load8(const T *src, int k, int n, bool vec, float (&v)[8])
+{
+    if (vec && k + 8 <= n) {
+        if constexpr (sizeof(T) == 2) {
+            const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(src + k));
+            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = __uint_as_float(a[j] << 16);
+                v[2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float4 w = __ldcg(reinterpret_cast<const float4 *>(src + k) + j);
+                v[4 * j] = w.x;
+                v[4 * j + 1] = w.y;
+                v[4 * j + 2] = w.z;
+                v[4 * j + 3] = w.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = k + j < n ? to_f32(__ldcg(src + k + j)) : 0.0f;
+    }
+}
+
+// 2^ex <= max < 2^(ex + 1) of a row whose largest magnitude has the bits
+// `top`; a row below 2^-112 counts as if its maximum were that, one with a
+// NaN or Inf (reported) as if no power were taken out.
+__device__ __forceinline__ int lin_exponent(uint32_t top)
+{
+    return top >= kNonFiniteBits ? 14 : max((int)(top >> 23), 15) - 127;
 }
 
 // ---------------------------------------------------------------------------
@@ -114,52 +178,18 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = nv * kVec + (int)threadIdx.x; i < n; i += kThreads)
         top = max(top, __float_as_uint(to_f32(__ldcg(src + i))) & 0x7FFFFFFFu);
     top = cta_max_u32(top);
-    const bool bad = top >= kNonFiniteBits;
-    if (bad && threadIdx.x == 0)
+    if (top >= kNonFiniteBits && threadIdx.x == 0)
         raise_status(status, kStatusNonFinite);
-    // 2^ex <= max < 2^(ex + 1); a row below 2^-112 counts as if its maximum were that
-    const int ex = bad ? 14 : max((int)(top >> 23), 15) - 127;
+    const int ex = lin_exponent(top);
     const float up = __uint_as_float((uint32_t)(127 + (14 - ex)) << 23);
     if (threadIdx.x < kParts)
         xe[to + (threadIdx.x ? per : 0)] = ex - 14 - (threadIdx.x ? 11 : 0);
     uint16_t *const dst = xh + to * Kpad, *const dst2 = dst + (int64_t)per * Kpad;
     for (int k = (int)threadIdx.x * 8; k < Kpad; k += kThreads * 8) {
         float v[8];
-        if (vec && k + 8 <= n) {
-            if constexpr (sizeof(T) == 2) {
-                const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(src + k));
-                const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[2 * j] = __uint_as_float(a[j] << 16);
-                    v[2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float4 w = __ldcg(reinterpret_cast<const float4 *>(src + k) + j);
-                    v[4 * j] = w.x;
-                    v[4 * j + 1] = w.y;
-                    v[4 * j + 2] = w.z;
-                    v[4 * j + 3] = w.w;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = k + j < n ? to_f32(__ldcg(src + k + j)) : 0.0f;
-        }
         uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float a = v[2 * j] * up, b = v[2 * j + 1] * up;
-            hi[j] = pack_f16x2(a, b);
-            if constexpr (kParts == 2) {
-                float ah, bh;
-                f16x2_to_f32(hi[j], ah, bh);
-                lo[j] = pack_f16x2((a - ah) * 2048.0f, (b - bh) * 2048.0f);
-            }
-        }
+        lin_load8(src, k, n, vec, v);
+        lin_terms<kParts>(v, up, hi, lo);
         *reinterpret_cast<uint4 *>(dst + k) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         if constexpr (kParts == 2)
             *reinterpret_cast<uint4 *>(dst2 + k) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -187,6 +217,9 @@ __device__ __forceinline__ void cluster_wait()
 }
 
 struct LinearArgs {
+    const void *x; // fused: the activations themselves
+    int64_t x_stride;
+    int K;
     const uint8_t *scales; // MMA layout, `tiles` 512-byte tiles per 128-row band
     const int32_t *xe;
     const float *g;
@@ -195,42 +228,113 @@ struct LinearArgs {
     int chunks, tiles, stages;
     int splits;       // CTAs of a cluster (grid x); grid y: tiles of columns, z: bands of the weight
     int share, more;  // chunks of a CTA, one more for the first `more`
+    int most_share;   // chunks that the fused layout's memory holds
     int own, own_inv; // weight rows that a CTA owns, and 2^16 / own rounded up
     int out_bf16;
     int32_t *status;
 };
 
-template <bool kNv>
+// The decoders' layout of a CTA's activations: every thread takes eights of
+// the rows; columns without a row are zeros.  Each element goes where a
+// 128-byte swizzled TMA copy of the packed row would have put it: per 64
+// elements a tile of 128-byte rows, 16-byte pieces XORed with the row's index
+// modulo 8.  The power of two taken out of a row is that of the CTA's share of
+// it, so nothing is exchanged between CTAs.
+template <typename T>
+__device__ __forceinline__ void lin_lay_out(const LinearArgs &a, uint8_t *x_area, float2 *factor, uint32_t *tops,
+                                            int c0, int n, int row0, int have, int groups, uint64_t *laid)
+{
+    constexpr int kParts = sizeof(T) == 4 ? 2 : 1, kAll = 32 * kLinDecoders;
+    const int tid = (int)threadIdx.x, lane = tid & 31;
+    const int k0 = c0 * kLinChunk, units = n * (kLinChunk / 8), end = a.K - k0;
+    auto at = [&](int u, int c) { return x_area + (u >> 3) * (a.cols * 128) + c * 128 + (((u & 7) ^ (c & 7)) * 16); };
+    for (int i = tid; i < n * a.cols * (kLinChunk * 2 / 16); i += kAll)
+        reinterpret_cast<uint4 *>(x_area)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < have)
+        tops[tid] = 0u;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    for (int m = 0; m < have; ++m) {
+        const T *src = static_cast<const T *>(a.x) + (int64_t)(row0 + m) * a.x_stride + k0;
+        const bool vec = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+        uint32_t top = 0;
+        for (int u = tid; u < units; u += kAll) {
+            float v[8];
+            lin_load8(src, u * 8, end, vec, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        }
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if (lane == 0)
+            atomicMax(&tops[m], top);
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    for (int m = 0; m < have; ++m) {
+        const T *src = static_cast<const T *>(a.x) + (int64_t)(row0 + m) * a.x_stride + k0;
+        const bool vec = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+        const int ex = lin_exponent(tops[m]);
+        const float up = __uint_as_float((uint32_t)(127 + (14 - ex)) << 23);
+        for (int u = tid; u < units; u += kAll) {
+            float v[8];
+            uint32_t hi[4], lo[4];
+            lin_load8(src, u * 8, end, vec, v);
+            lin_terms<kParts>(v, up, hi, lo);
+            *reinterpret_cast<uint4 *>(at(u, m)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (kParts == 2)
+                *reinterpret_cast<uint4 *>(at(u, groups + m)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        if (tid < kParts) {
+            const int e = ex - 14 - 11 * tid, e2 = e >> 1;
+            factor[tid * groups + m] = make_float2(exp2_int(e2), exp2_int(e - e2));
+            if (tops[m] >= kNonFiniteBits)
+                raise_status(a.status, kStatusNonFinite);
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); // the tensor core reads what was written
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(laid);
+}
+
+// T: the activations' type where the kernel lays them out itself, void where
+// they come packed.
+template <bool kNv, typename T>
 __global__ void __launch_bounds__(kLinThreads, 2)
     linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                   const LinearArgs a)
 {
     constexpr int kTiles = kNv ? 2 : 1; // scale tiles of a chunk
+    constexpr bool kFused = !std::is_void_v<T>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[kLinMaxStages], empty[kLinMaxStages], ready[kLinBuffers], done;
+    __shared__ __align__(8) uint64_t full[kLinMaxStages], empty[kLinMaxStages], ready[kLinBuffers], done, laid;
     __shared__ uint32_t tmem_slot;
     __shared__ float2 s_factor[kLinMaxCols]; // the column's power of two, in two factors
+    __shared__ uint32_t s_top[kLinFusedCols];
     __shared__ float s_g;
     __shared__ int consumed; // chunks whose copies the MMA warp has seen land
     uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
     const int splits = a.splits, split = (int)blockIdx.x, mtile = (int)blockIdx.y, band = (int)blockIdx.z;
     const int c0 = split * a.share + min(split, a.more), n = a.share + (split < a.more ? 1 : 0);
-    const int stages = a.stages, stage_bytes = lin_stage_bytes(a.cols);
+    const int stages = a.stages, stage_bytes = lin_stage_bytes(a.cols, kFused);
     const uint32_t tmem_cols = (uint32_t)lin_tmem_cols(a.cols);
 
-    // Copies.  The weight is no work of the packing grid's, which runs only
-    // once everything before it is done: the first stages of it are asked for
-    // before that grid ends, the activations after.
+    uint8_t *const x_area = smem + stages * stage_bytes; // fused: [chunk][two tiles of 64 elements]
+    // Copies.  Where a packing grid precedes this one, it runs only once
+    // everything before it is done, and the weight is no work of its: the first
+    // stages of the weight are asked for before that grid ends, the
+    // activations after.
     auto weight = [&](int i, int s) {
         const int c = c0 + i;
         uint8_t *const st = smem + s * stage_bytes;
         const uint32_t scale_bytes = (uint32_t)min(kTiles, a.tiles - c * kTiles) * 512u;
-        mbar_expect_tx(&full[s], (uint32_t)(kLinCodes + a.cols * kLinChunk * 2) + scale_bytes);
+        mbar_expect_tx(&full[s], (uint32_t)(stage_bytes - kLinScales) + scale_bytes);
         tma_load_2d(st, &map_w, c * (kLinChunk / 2), band * kLinRows, &full[s]);
         bulk_load(st + kLinCodes, a.scales + ((int64_t)band * a.tiles + (int64_t)c * kTiles) * 512, scale_bytes, &full[s]);
     };
     auto activations = [&](int i, int s) {
+        if constexpr (kFused)
+            return;
         const int c = c0 + i;
         uint8_t *const st = smem + s * stage_bytes + kLinCodes + kLinScales;
         tma_load_2d(st, &map_x, c * kLinChunk, mtile * a.cols, &full[s]);
@@ -238,6 +342,8 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     };
     const int first = n < stages ? n : stages;
     const int groups = a.cols / a.parts, have = min(groups, a.rows - mtile * groups); // activation rows of the tile
+    if constexpr (kFused)
+        pdl_begin();
     cluster_arrive(); // this CTA runs: the others may write to its shared memory
     if (warp == kLinDecoders && elect_one()) {
         for (int s = 0; s < stages; ++s) {
@@ -247,6 +353,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
         for (int i = 0; i < kLinBuffers; ++i)
             mbar_init(&ready[i], kLinDecoders / 2);
         mbar_init(&done, 1);
+        mbar_init(&laid, kLinDecoders);
         mbar_init_fence();
         consumed = 0;
         weight(0, 0); // the others once the rest of the CTA may go on
@@ -297,18 +404,23 @@ __global__ void __launch_bounds__(kLinThreads, 2)
         // a test of the lane: the compiler then knows that one thread issues and
         // keeps the descriptors in uniform registers (measured alone at N = 16:
         // 10 cycles per MMA against 46).
-        pdl_begin();
-        for (int i = lane; i < a.cols; i += 32) { // for the epilogue
-            const int e = __ldcg(a.xe + mtile * a.cols + i), e2 = e >> 1;
-            s_factor[i] = make_float2(exp2_int(e2), exp2_int(e - e2));
+        if constexpr (!kFused) {
+            pdl_begin();
+            for (int i = lane; i < a.cols; i += 32) { // for the epilogue
+                const int e = __ldcg(a.xe + mtile * a.cols + i), e2 = e >> 1;
+                s_factor[i] = make_float2(exp2_int(e2), exp2_int(e - e2));
+            }
         }
         if (kNv && lane == 0)
             s_g = __ldcg(a.g);
         const uint32_t idesc = (1u << 4) | ((uint32_t)(a.cols / 8) << 17) | ((uint32_t)(kLinRows / 16) << 24);
-        const uint64_t x0 = smem_desc_sw128(smem_addr(smem + kLinCodes + kLinScales));
-        const uint32_t half = (uint32_t)a.cols * kLinChunk / 16, step = (uint32_t)stage_bytes / 16; // in descriptor units
+        const uint64_t x0 = smem_desc_sw128(smem_addr(kFused ? x_area : smem + kLinCodes + kLinScales));
+        // in descriptor units of 16 bytes
+        const uint32_t half = (uint32_t)a.cols * kLinChunk / 16, step = kFused ? 2 * half : (uint32_t)stage_bytes / 16;
+        if (kFused && !__all_sync(0xFFFFFFFFu, mbar_wait(&laid, 0)))
+            timed_out = true;
         uint32_t phase = 0, ready_phase = 0;
-        for (int i = 0, s = 0, b = 0; i < n; ++i) {
+        for (int i = 0, s = 0, b = 0; i < n && !timed_out; ++i) {
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[s], phase))) {
                 timed_out = true;
                 break;
@@ -321,7 +433,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
             }
             tc_fence_after();
             if (elect_one()) {
-                const uint64_t x = x0 + (uint64_t)((uint32_t)s * step);
+                const uint64_t x = x0 + (uint64_t)((uint32_t)(kFused ? i : s) * step);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     tc_mma_f16_ts(tmem, tmem_a + (uint32_t)(64 * b + 8 * k),
@@ -344,6 +456,8 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     } else {
         const int group = warp >> 2, quarter = warp & 3; // rows 32 quarter .. + 31: the tensor-memory lanes this warp reaches
         const int row = quarter * 32 + lane, word = lane * 16 + quarter * 4; // its scale word in a tile
+        if constexpr (kFused)
+            lin_lay_out<T>(a, x_area, s_factor, s_top, c0, n, mtile * groups, have, groups, &laid);
         if constexpr (!kNv) {
             const uint8_t *p = a.scales + ((int64_t)band * a.tiles + c0) * 512 + word;
             uint32_t m4 = 0;
@@ -424,7 +538,8 @@ __global__ void __launch_bounds__(kLinThreads, 2)
             if (b >= kLinBuffers)
                 b -= kLinBuffers;
         }
-        pdl_begin(); // what is read and written below follows the packing grid
+        if constexpr (!kFused)
+            pdl_begin(); // what is read and written below follows the packing grid
     }
 
     // ---- the sums, times g or 2^E and the column's power of two, to the CTA that owns the row ----
@@ -434,7 +549,9 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     if (warp == kLinDecoders) // copies that nobody waited for (only after a timeout) land before the CTA ends
         for (int i = consumed; i < issued; ++i)
             (void)mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u);
-    float *const land = reinterpret_cast<float *>(smem + (a.cols <= kLinLandingCols ? stages * stage_bytes : 0)); // [CTA][column][its rows]
+    float *const land = reinterpret_cast<float *>(
+        smem + (a.cols <= kLinLandingCols ? stages * stage_bytes + (kFused ? a.most_share * a.cols * kLinChunk * 2 : 0) : 0));
+    // (land: [CTA][column][its rows])
     cluster_wait(); // every CTA of the cluster runs
     if (a.cols > kLinLandingCols) {
         cluster_arrive();
