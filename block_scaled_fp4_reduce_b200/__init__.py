@@ -11,7 +11,6 @@ outputs and return them.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 import os
@@ -565,17 +564,28 @@ def _cuda(t: torch.Tensor, what: str, dtype=None):
     return t
 
 
-def _on(device: torch.device):
-    """Makes `device` the current one for a call; the library launches on the current device."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# The current stream's handle without building a Stream object (3 us of the 5 us that a call of the library
+# takes); torch.cuda.current_stream where torch does not offer it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _same_device(device, *tensors):
+def _call(name: str, index: int, stream, *args) -> None:
+    """The entry point `name` on device `index` (the library launches on the
+    current device), on `stream` or that device's current stream."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _call(name, index, stream, *args)
+    s = _raw_stream(index) if stream is None else _stream(stream)
+    st = getattr(_lib, name)(*args, s)
+    if st != OK:
+        raise FP4Error(st, name)
+
+
+def _same_device(index: int, *tensors) -> None:
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors of a call live on one device: {device} and {t.device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors of a call live on one device: cuda:{index} and {t.device}")
 
 
 class KVCacheStruct(ctypes.Structure):
@@ -599,8 +609,8 @@ class KVCache:
         if fmt not in (NVFP4, MXFP4):
             raise ValueError("fmt: NVFP4 or MXFP4")
         group = 16 if fmt == NVFP4 else 32
-        dev = _cuda(k_packed, "k_packed").device
-        _same_device(dev, k_scales, v_packed, v_scales, status)
+        dev, self.index = _cuda(k_packed, "k_packed").device, k_packed.get_device()
+        _same_device(self.index, k_scales, v_packed, v_scales, status)
         for name, t in (("k_packed", k_packed), ("k_scales", k_scales), ("v_packed", v_packed), ("v_scales", v_scales)):
             if t.dtype != torch.uint8 or t.dim() != 4 or not t.is_contiguous():
                 raise ValueError(f"{name}: contiguous uint8 [pages, heads, page_size, bytes] required")
@@ -613,7 +623,7 @@ class KVCache:
             for name, g in (("k_global_scale", k_global_scale), ("v_global_scale", v_global_scale)):
                 if g is None or g.dtype != torch.float32 or g.shape != (self.heads,) or not g.is_contiguous():
                     raise ValueError(f"{name}: contiguous float32 [heads] required for NVFP4")
-            _same_device(dev, k_global_scale, v_global_scale)
+            _same_device(self.index, k_global_scale, v_global_scale)
         self.fmt, self.device = fmt, dev
         self.k_packed, self.k_scales, self.v_packed, self.v_scales = k_packed, k_scales, v_packed, v_scales
         self.k_global_scale, self.v_global_scale = k_global_scale, v_global_scale
@@ -623,6 +633,7 @@ class KVCache:
                                      _p(k_scales), _p(v_packed), _p(v_scales), _p(k_global_scale) if nv else None,
                                      _p(v_global_scale) if nv else None)
         self._ref = ctypes.addressof(self._struct)
+        lib()
 
     def check(self, where: str = "KVCache"):
         st = int(self.status.item())
@@ -654,9 +665,16 @@ def _token_rows(t: torch.Tensor, what: str, tokens: int, heads: int, dim: int) -
     """Token stride of a [tokens, heads, dim] tensor whose heads and elements are contiguous."""
     if t.shape != (tokens, heads, dim):
         raise ValueError(f"{what}: [{tokens}, {heads}, {dim}] required, got {list(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+    one, head, el = t.stride()
+    if tokens and (el != 1 or (heads > 1 and head != dim)):
         raise ValueError(f"{what}: contiguous heads and elements required")
-    return t.stride(0) if tokens > 1 else heads * dim
+    return one if tokens > 1 else heads * dim
+
+
+def _slot_list(slots: torch.Tensor) -> int:
+    if slots.dtype != torch.int64 or not slots.is_cuda or not slots.is_contiguous():
+        raise ValueError("slots: a contiguous int64 CUDA tensor required")
+    return slots.numel()
 
 
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rule: int = MX_FLOOR, status=None,
@@ -665,34 +683,31 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     projection may keep their token stride) into the cache's `slots` (int64
     [tokens], negative = padding).  Data errors go to `status` (default: the
     cache's)."""
-    T = slots.numel()
-    _cuda(slots, "slots", torch.int64)
-    if k.dtype != v.dtype or not slots.is_contiguous():
-        raise ValueError("k and v share one dtype; slots contiguous")
-    ks, vs = (_token_rows(t, n, T, cache.heads, cache.head_dim) for t, n in ((k, "k"), (v, "v")))
-    st = status if status is not None else cache.status
-    _same_device(cache.device, k, v, slots, st)
-    with _on(cache.device):
-        _check(lib().fp4_kv_write(cache._ref, _p(k), _p(v), _dtype_code(k), T, ks, vs, _p(slots), rule, _p(st),
-                                  _stream(stream)), "fp4_kv_write")
+    T, H, D = _slot_list(slots), cache.heads, cache.head_dim
+    if k.dtype != v.dtype:
+        raise TypeError("k and v share one dtype")
+    ks, vs = _token_rows(k, "k", T, H, D), _token_rows(v, "v", T, H, D)
+    st = cache.status if status is None else status
+    _same_device(cache.index, k, v, slots, status)
+    _call("fp4_kv_write", cache.index, stream, cache._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k), T, ks, vs,
+          slots.data_ptr(), rule, st.data_ptr())
 
 
 def kv_read(cache: KVCache, slots: torch.Tensor, out_dtype=torch.bfloat16, k=None, v=None, status=None, stream=None):
     """The keys and values in `slots` (int64 [tokens]; negative gives zeros)
     as [tokens, heads, head_dim] tensors of out_dtype, or into k and v."""
-    T = slots.numel()
-    _cuda(slots, "slots", torch.int64)
-    shape = (T, cache.heads, cache.head_dim)
-    k = torch.empty(shape, dtype=out_dtype, device=cache.device) if k is None else k
-    v = torch.empty(shape, dtype=k.dtype, device=cache.device) if v is None else v
-    if k.dtype != v.dtype or not slots.is_contiguous():
-        raise ValueError("k and v share one dtype; slots contiguous")
-    ks, vs = (_token_rows(t, n, *shape) for t, n in ((k, "k"), (v, "v")))
-    st = status if status is not None else cache.status
-    _same_device(cache.device, k, v, slots, st)
-    with _on(cache.device):
-        _check(lib().fp4_kv_read(cache._ref, _p(slots), T, _p(k), _p(v), _dtype_code(k), ks, vs, _p(st),
-                                 _stream(stream)), "fp4_kv_read")
+    T, H, D = _slot_list(slots), cache.heads, cache.head_dim
+    if k is None:
+        k = torch.empty((T, H, D), dtype=out_dtype, device=cache.device)
+    if v is None:
+        v = torch.empty((T, H, D), dtype=k.dtype, device=cache.device)
+    if k.dtype != v.dtype:
+        raise TypeError("k and v share one dtype")
+    ks, vs = _token_rows(k, "k", T, H, D), _token_rows(v, "v", T, H, D)
+    st = cache.status if status is None else status
+    _same_device(cache.index, k, v, slots, status)
+    _call("fp4_kv_read", cache.index, stream, cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
+          _dtype_code(k), ks, vs, st.data_ptr())
     return k, v
 
 
@@ -715,32 +730,30 @@ def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_
     if q.dim() != 4 or q.shape[3] != cache.head_dim:
         raise ValueError(f"q: [batch, q_tokens, q_heads, {cache.head_dim}] required, got {list(q.shape)}")
     B, L, HQ, D = q.shape
-    _cuda(page_table, "page_table", torch.int32)
-    _cuda(seq_lens, "seq_lens", torch.int32)
-    if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape != (B,):
-        raise ValueError(f"page_table [{B}, width] and seq_lens [{B}] required")
-    if not page_table.is_contiguous() or not seq_lens.is_contiguous():
-        raise ValueError("page_table and seq_lens: contiguous tensors required")
-    if q.numel():
-        one = q.stride(1) if L > 1 else q.stride(0) if B > 1 else HQ * D
-        if q.stride(3) != 1 or (HQ > 1 and q.stride(2) != D) or (B > 1 and q.stride(0) != one * L):
-            raise ValueError("q: contiguous heads and elements and one stride from token to token required")
-    else:
+    for what, t, dims in (("page_table", page_table, 2), ("seq_lens", seq_lens, 1)):
+        if t.dtype != torch.int32 or t.dim() != dims or t.size(0) != B or not t.is_contiguous():
+            raise ValueError(f"{what}: contiguous int32 [{B}{', width' if dims == 2 else ''}] required")
+    if q.is_contiguous():
         one = HQ * D
-    out = torch.empty((B, L, HQ, D), dtype=q.dtype, device=q.device) if out is None else out
-    lse = torch.empty((B, L, HQ), dtype=torch.float32, device=q.device) if lse is None else lse
-    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+    else:
+        sb, sl, sh, el = q.stride()
+        one = sl if L > 1 else sb if B > 1 else HQ * D
+        if el != 1 or (HQ > 1 and sh != D) or (B > 1 and sb != one * L):
+            raise ValueError("q: contiguous heads and elements and one stride from token to token required")
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out: contiguous, with q's shape and dtype")
-    if lse.shape != (B, L, HQ) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    if lse is None:
+        lse = torch.empty((B, L, HQ), dtype=torch.float32, device=q.device)
+    elif lse.shape != (B, L, HQ) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse: contiguous float32 [batch, q_tokens, q_heads]")
-    ws = workspace if workspace is not None else kv_attention_workspace(q, cache, page_table)
-    st = status if status is not None else cache.status
-    _same_device(cache.device, q, page_table, seq_lens, out, lse, ws, st)
-    with _on(cache.device):
-        _check(lib().fp4_kv_attention(cache._ref, _p(q), _dtype_code(q), B, L, HQ, one, _p(page_table),
-                                      page_table.shape[1], _p(seq_lens), D ** -0.5 if scale is None else scale,
-                                      window, _p(out), _p(lse), _p(ws), ws.numel() * ws.element_size(), _p(st),
-                                      _stream(stream)), "fp4_kv_attention")
+    ws = kv_attention_workspace(q, cache, page_table) if workspace is None else workspace
+    st = cache.status if status is None else status
+    _same_device(cache.index, q, page_table, seq_lens, out, lse, ws, status)
+    _call("fp4_kv_attention", cache.index, stream, cache._ref, q.data_ptr(), _dtype_code(q), B, L, HQ, one,
+          page_table.data_ptr(), page_table.size(1), seq_lens.data_ptr(), D ** -0.5 if scale is None else scale, window,
+          out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), st.data_ptr())
     return out, lse
 
 
@@ -754,7 +767,7 @@ class LinearWeight:
         kp = _padded(k, group)
         if fmt not in (NVFP4, MXFP4):
             raise ValueError("fmt: NVFP4 or MXFP4")
-        dev = _cuda(packed, "packed", torch.uint8).device
+        dev, self.index = _cuda(packed, "packed", torch.uint8).device, packed.get_device()
         _cuda(scales_mma, "scales_mma", torch.uint8)
         if packed.numel() != n * kp // 2 or not packed.is_contiguous():
             raise ValueError(f"packed: contiguous [{n}, {kp // 2}] required")
@@ -762,9 +775,10 @@ class LinearWeight:
             raise ValueError("scales_mma: the MMA layout of the [n, Kp/G] scales required (scales_to_mma)")
         if fmt == NVFP4 and (global_scale is None or global_scale.dtype != torch.float32 or global_scale.numel() != 1):
             raise ValueError("global_scale: one float32 required for NVFP4")
-        _same_device(dev, scales_mma, global_scale, status)
+        _same_device(self.index, scales_mma, global_scale if fmt == NVFP4 else None, status)
         self.fmt, self.n, self.k, self.device = fmt, n, k, dev
         self.packed, self.scales_mma, self.global_scale = packed, scales_mma, global_scale
+        self._packed, self._scales, self._g = _p(packed), _p(scales_mma), _p(global_scale) if fmt == NVFP4 else None
         self.status = status if status is not None else new_status(dev)
 
     def check(self, where: str = "LinearWeight"):
@@ -790,26 +804,28 @@ def linear(x: torch.Tensor, w: LinearWeight, out_dtype=None, out=None, workspace
     """y [..., n] = x [..., k] W^T for a few rows of unquantised activations
     (bf16 or fp32; rows of a 2-D x may be strided) and an FP4 weight.
     out_dtype: x's by default."""
-    if x.dim() == 0 or x.shape[-1] != w.k:
-        raise ValueError(f"x: [..., {w.k}] required, got {list(x.shape)}")
-    rows = x.numel() // w.k if w.k else x.shape[:-1].numel()
-    if x.dim() == 2 and (x.stride(1) == 1 or w.k <= 1):
-        stride = x.stride(0) if rows > 1 else w.k
-    elif x.is_contiguous():
+    shape = x.shape
+    if not shape or shape[-1] != w.k:
+        raise ValueError(f"x: [..., {w.k}] required, got {list(shape)}")
+    rows = shape[:-1].numel()
+    if x.is_contiguous():
         stride = w.k
+    elif x.dim() == 2 and (x.stride(1) == 1 or w.k == 1):
+        stride = x.stride(0) if rows > 1 else w.k
     else:
         raise ValueError("x: contiguous elements required, and contiguous rows beyond two dimensions")
-    shape = (*x.shape[:-1], w.n)
-    y = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device) if out is None else out
-    if y.shape != shape or not y.is_contiguous():
-        raise ValueError(f"out: contiguous {list(shape)} required")
-    ws = workspace if workspace is not None else linear_workspace(rows, w)
-    st = status if status is not None else w.status
-    _same_device(w.device, x, y, ws, st)
-    with _on(w.device):
-        _check(lib().fp4_linear(w.fmt, _p(x), _dtype_code(x), rows, w.k, stride, _p(w.packed), _p(w.scales_mma),
-                                _p(w.global_scale), w.n, _p(y), _dtype_code(y), _p(ws),
-                                ws.numel() * ws.element_size(), _p(st), _stream(stream)), "fp4_linear")
+    if out is None:
+        y = torch.empty((*shape[:-1], w.n), dtype=out_dtype or x.dtype, device=w.device)
+    else:
+        y = out
+        if y.shape != (*shape[:-1], w.n) or not y.is_contiguous() or (out_dtype is not None and y.dtype != out_dtype):
+            raise ValueError(f"out: contiguous {[*shape[:-1], w.n]} of the output dtype required")
+    ws = linear_workspace(rows, w) if workspace is None else workspace
+    st = w.status if status is None else status
+    _same_device(w.index, x, y, ws, status)
+    _call("fp4_linear", w.index, stream, w.fmt, x.data_ptr(), _dtype_code(x), rows, w.k, stride, w._packed,
+          w._scales, w._g, w.n, y.data_ptr(), _dtype_code(y), ws.data_ptr(), ws.numel() * ws.element_size(),
+          st.data_ptr())
     return y
 
 
