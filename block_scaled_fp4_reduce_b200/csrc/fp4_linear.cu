@@ -34,7 +34,7 @@ fp4_status matrix_map(CUtensorMapDataType type, int size, const void *p, int64_t
 }
 
 // Workspace: the activations as fp16 rows [tiles * cols][Kpad], then an
-// exponent for each.
+// exponent for each of them and share of K.
 struct Layout {
     int cols, chunks; // columns of a tile (activation rows x parts, whole sixteens)
     int64_t tiles, Kpad;
@@ -53,7 +53,7 @@ Layout layout(int64_t rows, int64_t K, int parts)
     l.chunks = (int)((K + fp4::kLinChunk - 1) / fp4::kLinChunk);
     l.Kpad = (int64_t)l.chunks * fp4::kLinChunk;
     l.xh = (size_t)(l.tiles * l.cols * l.Kpad) * 2;
-    l.bytes = l.xh + (size_t)(l.tiles * l.cols) * sizeof(int32_t);
+    l.bytes = l.xh + (size_t)(l.tiles * l.cols) * fp4::kLinMaxSplits * sizeof(int32_t);
     return l;
 }
 
@@ -96,11 +96,10 @@ fp4_status launch_linear(const CUtensorMap &map_w, const CUtensorMap &map_x, fp4
     auto kernel = fp4::linear_kernel<kNv, T>;
     if (!smem_attr(kernel, 224 * 1024))
         return FP4_ERR_CUDA;
-    a.share = a.chunks / a.splits;
-    a.more = a.chunks % a.splits;
     a.most_share = a.share + (a.more > 0);
     a.own = (fp4::kLinRows + a.splits - 1) / a.splits;
     a.own_inv = (65536 + a.own - 1) / a.own;
+    a.own_magic = (uint32_t)((0x100000000ull + a.own - 1) / a.own);
     cudaLaunchConfig_t cfg = {};
     a.stages = pick_stages(a.cols, std::is_void_v<T> ? 0 : a.most_share, cfg.dynamicSmemBytes);
     cfg.gridDim = dim3((unsigned)a.splits, (unsigned)mtiles, (unsigned)bands);
@@ -205,6 +204,8 @@ fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t ro
     a.out_bf16 = out_dtype == FP4_BF16;
     a.status = status;
     a.splits = pick_splits(bands * l.tiles, a.chunks, (int64_t)sms * (a.cols <= fp4::kLinSharedCols ? 2 : 1));
+    a.share = a.chunks / a.splits;
+    a.more = a.chunks % a.splits;
     const bool bf = dtype == FP4_BF16, nv = fmt == FP4_NVFP4;
     const int share = (a.chunks + a.splits - 1) / a.splits;
     if (a.cols <= fp4::kLinFusedCols && share <= fp4::kLinFusedShare && rows * share <= fp4::kLinFusedWork) {
@@ -221,11 +222,13 @@ fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t ro
                     CU_TENSOR_MAP_SWIZZLE_128B, &map_x);
     if (st != FP4_OK)
         return st;
-    const int per = l.cols / parts, packed_rows = (int)(l.tiles * per), Kpad = (int)l.Kpad;
-    st = bf ? launch(fp4::linear_pack_kernel<uint16_t>, packed_rows, stream, static_cast<const uint16_t *>(x), (int)rows,
-                     (int)K, x_stride, per, Kpad, xh, xe, status)
-            : launch(fp4::linear_pack_kernel<float>, packed_rows, stream, static_cast<const float *>(x), (int)rows, (int)K,
-                     x_stride, per, Kpad, xh, xe, status);
+    const int per = l.cols / parts, Kpad = (int)l.Kpad;
+    const dim3 grid((unsigned)(l.tiles * per), (unsigned)a.splits);
+    st = bf ? launch_cfg(fp4::linear_pack_kernel<uint16_t>, grid, fp4::kThreads, 0, stream,
+                         static_cast<const uint16_t *>(x), (int)rows, (int)K, x_stride, per, Kpad, a.share, a.more, xh, xe,
+                         status)
+            : launch_cfg(fp4::linear_pack_kernel<float>, grid, fp4::kThreads, 0, stream, static_cast<const float *>(x),
+                         (int)rows, (int)K, x_stride, per, Kpad, a.share, a.more, xh, xe, status);
     if (st != FP4_OK)
         return st;
     return nv ? launch_linear<true, void>(map_w, map_x, a, l.tiles, bands, stream)

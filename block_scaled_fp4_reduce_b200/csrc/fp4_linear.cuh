@@ -11,7 +11,7 @@
 //                       but for what lies 2^-38 below the maximum; fp32 x: two
 //                       terms, 22 bits, in two rows)
 //   linear_kernel       a cluster of `splits` CTAs per 128 weight rows and up
-//                       to 256 columns (activation rows, or terms of them);
+//                       to 160 columns (activation rows, or terms of them);
 //                       each CTA takes a share of K in chunks of 128 elements
 //                       through a ring filled by TMA; each row's partial sums
 //                       are written to the CTA of the cluster that owns the
@@ -51,18 +51,19 @@ constexpr int kLinDecoders = 8;        // warps
 constexpr int kLinThreads = 32 * (kLinDecoders + 2);
 constexpr int kLinCodes = kLinRows * kLinChunk / 2; // 8 KB
 constexpr int kLinScales = 1024;       // two 512-byte scale tiles (NVFP4; MXFP4 has one)
-constexpr int kLinMaxCols = 256;
+constexpr int kLinMaxCols = 160; // two part areas (below) have to fit in the ring
 constexpr int kLinMaxStages = 8;
 constexpr int kLinMaxSplits = 8;
 
-// Partial sums of the rows that a CTA owns, from every CTA of the cluster: in
-// memory of their own up to 32 columns, beyond that in the ring, which then
-// costs a barrier more (every CTA has to be done with its ring).
+// Partial sums: a CTA's own 128 rows on their way out, [owner][column][row],
+// which take the ring's place, and those of the rows that it owns as they come
+// in, [CTA][column][row], which have memory of their own up to 32 columns and
+// follow the others in the ring's place beyond that, at the cost of a barrier
+// more (every CTA has to be done with its ring).
 constexpr int kLinLandingCols = 32;
-__host__ __device__ constexpr int lin_landing_bytes(int cols)
-{
-    return cols <= kLinLandingCols ? cols * 4 * (kLinRows + kLinMaxSplits) : 0;
-}
+__host__ __device__ constexpr int lin_part_bytes(int cols) { return cols * 4 * (kLinRows + kLinMaxSplits); }
+__host__ __device__ constexpr int lin_landing_bytes(int cols) { return cols <= kLinLandingCols ? lin_part_bytes(cols) : 0; }
+
 // Where a CTA's share of the activations is small, the decoders lay it out
 // themselves, in shared memory, while the first codes are on their way: no
 // packing grid and no workspace.  The most columns, chunks of K, and rows x
@@ -142,57 +143,56 @@ __device__ __forceinline__ int lin_exponent(uint32_t top)
 }
 
 // ---------------------------------------------------------------------------
-// One CTA per activation row, padding rows of the last tile among them (zeros).
-// xh: fp16 [tiles * cols][Kpad]; a tile holds `per` rows and, for fp32 x,
-// their second terms in the rows `per` on.  xe [tiles * cols]: the exponent of
-// the power of two that each of them is to be multiplied by.
+// One CTA per activation row (padding rows of the last tile among them: zeros)
+// and share of K, which are those of the product's CTAs: the power of two taken
+// out of a row is that of the share, so that nothing is exchanged between CTAs
+// and the elements are read once.  xh: fp16 [tiles * cols][Kpad]; a tile holds
+// `per` rows and, for fp32 x, their second terms in the rows `per` on.  xe
+// [tiles][shares][cols]: the exponent of the power of two that each of them is
+// to be multiplied by.
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    linear_pack_kernel(const T *__restrict__ x, int rows, int K, int64_t x_stride, int per, int Kpad, uint16_t *xh,
-                       int32_t *xe, int32_t *status)
+    linear_pack_kernel(const T *__restrict__ x, int rows, int K, int64_t x_stride, int per, int Kpad, int share, int more,
+                       uint16_t *xh, int32_t *xe, int32_t *status)
 {
     pdl_begin();
     // the product may start: it waits for this grid before it reads what is written here
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
-    const int row = (int)blockIdx.x, tile = row / per;
-    const int64_t to = (int64_t)tile * per * kParts + (row - tile * per);
-    const T *src = x + (int64_t)row * x_stride;
-    const int n = row < rows ? K : 0;
+    const int row = (int)blockIdx.x, tile = row / per, split = (int)blockIdx.y, splits = (int)gridDim.y;
+    const int k0 = (split * share + min(split, more)) * kLinChunk, len = (share + (split < more ? 1 : 0)) * kLinChunk;
+    const T *src = x + (int64_t)row * x_stride + k0;
+    const int n = row < rows ? K - k0 : 0; // elements there are, from k0 on
     const bool vec = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
-    constexpr int kVec = 16 / (int)sizeof(T);
+    float keep[8]; // the thread's first eight; a share beyond 2048 elements is read again
     uint32_t top = 0;
-    const int nv = vec ? n / kVec : 0;
-    for (int i = (int)threadIdx.x; i < nv; i += kThreads) {
-        const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(src) + i);
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+    for (int u = (int)threadIdx.x; u < len / 8; u += kThreads) {
+        float v[8];
+        lin_load8(src, u * 8, n, vec, v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (sizeof(T) == 2)
-                top = max(top, max((a[j] << 16) & 0x7FFF0000u, a[j] & 0x7FFF0000u));
-            else
-                top = max(top, a[j] & 0x7FFFFFFFu);
+        for (int j = 0; j < 8; ++j) {
+            top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+            if (u < kThreads)
+                keep[j] = v[j];
         }
     }
-    for (int i = nv * kVec + (int)threadIdx.x; i < n; i += kThreads)
-        top = max(top, __float_as_uint(to_f32(__ldcg(src + i))) & 0x7FFFFFFFu);
     top = cta_max_u32(top);
     if (top >= kNonFiniteBits && threadIdx.x == 0)
         raise_status(status, kStatusNonFinite);
-    const int ex = lin_exponent(top);
+    const int ex = lin_exponent(top), at = row - tile * per;
     const float up = __uint_as_float((uint32_t)(127 + (14 - ex)) << 23);
     if (threadIdx.x < kParts)
-        xe[to + (threadIdx.x ? per : 0)] = ex - 14 - (threadIdx.x ? 11 : 0);
-    uint16_t *const dst = xh + to * Kpad, *const dst2 = dst + (int64_t)per * Kpad;
-    for (int k = (int)threadIdx.x * 8; k < Kpad; k += kThreads * 8) {
-        float v[8];
+        xe[(tile * splits + split) * per * kParts + at + (threadIdx.x ? per : 0)] = ex - 14 - (threadIdx.x ? 11 : 0);
+    uint16_t *const dst = xh + ((int64_t)tile * per * kParts + at) * Kpad + k0, *const dst2 = dst + (int64_t)per * Kpad;
+    for (int u = (int)threadIdx.x; u < len / 8; u += kThreads) {
         uint32_t hi[4], lo[4];
-        lin_load8(src, k, n, vec, v);
-        lin_terms<kParts>(v, up, hi, lo);
-        *reinterpret_cast<uint4 *>(dst + k) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (u >= kThreads)
+            lin_load8(src, u * 8, n, vec, keep);
+        lin_terms<kParts>(keep, up, hi, lo);
+        *reinterpret_cast<uint4 *>(dst + u * 8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         if constexpr (kParts == 2)
-            *reinterpret_cast<uint4 *>(dst2 + k) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4 *>(dst2 + u * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
 }
 
@@ -229,7 +229,8 @@ struct LinearArgs {
     int splits;       // CTAs of a cluster (grid x); grid y: tiles of columns, z: bands of the weight
     int share, more;  // chunks of a CTA, one more for the first `more`
     int most_share;   // chunks that the fused layout's memory holds
-    int own, own_inv; // weight rows that a CTA owns, and 2^16 / own rounded up
+    int own, own_inv;   // weight rows that a CTA owns, and 2^16 / own rounded up
+    uint32_t own_magic; // 2^32 / own rounded up (own = 1 does not occur)
     int out_bf16;
     int32_t *status;
 };
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     constexpr int kTiles = kNv ? 2 : 1; // scale tiles of a chunk
     constexpr bool kFused = !std::is_void_v<T>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[kLinMaxStages], empty[kLinMaxStages], ready[kLinBuffers], done, laid;
+    __shared__ __align__(8) uint64_t full[kLinMaxStages], empty[kLinMaxStages], ready[kLinBuffers], done, laid, landed;
     __shared__ uint32_t tmem_slot;
     __shared__ float2 s_factor[kLinMaxCols]; // the column's power of two, in two factors
     __shared__ uint32_t s_top[kLinFusedCols];
@@ -344,7 +345,6 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     const int groups = a.cols / a.parts, have = min(groups, a.rows - mtile * groups); // activation rows of the tile
     if constexpr (kFused)
         pdl_begin();
-    cluster_arrive(); // this CTA runs: the others may write to its shared memory
     if (warp == kLinDecoders && elect_one()) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], 1);
@@ -354,8 +354,10 @@ __global__ void __launch_bounds__(kLinThreads, 2)
             mbar_init(&ready[i], kLinDecoders / 2);
         mbar_init(&done, 1);
         mbar_init(&laid, kLinDecoders);
+        mbar_init(&landed, 1);
         mbar_init_fence();
         consumed = 0;
+        mbar_expect_tx(&landed, (uint32_t)(splits * a.cols * a.own * 4));
         weight(0, 0); // the others once the rest of the CTA may go on
     }
     __syncwarp();
@@ -365,6 +367,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot, tmem_a = tmem + (uint32_t)a.cols;
+    cluster_arrive(); // this CTA runs, its barriers are there: the others may copy into its shared memory
 
     bool timed_out = false;
     int issued = 0;
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
         if constexpr (!kFused) {
             pdl_begin();
             for (int i = lane; i < a.cols; i += 32) { // for the epilogue
-                const int e = __ldcg(a.xe + mtile * a.cols + i), e2 = e >> 1;
+                const int e = __ldcg(a.xe + (mtile * splits + split) * a.cols + i), e2 = e >> 1;
                 s_factor[i] = make_float2(exp2_int(e2), exp2_int(e - e2));
             }
         }
@@ -549,65 +552,81 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     if (warp == kLinDecoders) // copies that nobody waited for (only after a timeout) land before the CTA ends
         for (int i = consumed; i < issued; ++i)
             (void)mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u);
+    float *const part = reinterpret_cast<float *>(smem);
     float *const land = reinterpret_cast<float *>(
-        smem + (a.cols <= kLinLandingCols ? stages * stage_bytes + (kFused ? a.most_share * a.cols * kLinChunk * 2 : 0) : 0));
-    // (land: [CTA][column][its rows])
+        smem + (a.cols > kLinLandingCols ? lin_part_bytes(a.cols)
+                                         : stages * stage_bytes + (kFused ? a.most_share * a.cols * kLinChunk * 2 : 0)));
+    __syncthreads();
+    if (warp < kLinDecoders) {
+        tc_fence_after();
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const int owner = (row * a.own_inv) >> 16; // row / own
+        float *const to = part + owner * (a.cols - 1) * a.own + row; // [owner][column][row - owner * own]
+        // The row's factor (g, or 2^E) between the two halves of the column's:
+        // neither alone need keep a sum inside fp32's range that both together
+        // leave there.
+        const float r = kNv ? s_g : e8m0_to_f32(top);
+        for (int c = (warp >> 2) * 8; c < a.cols; c += 16) {
+            if (c >= have && (a.parts == 1 || c < groups || c >= groups + have))
+                continue; // columns without a row
+            float v[8];
+            tc_load_8(tmem + (uint32_t)c + ((uint32_t)(quarter * 32) << 16), v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 f = s_factor[c + j];
+                to[(c + j) * a.own] = v[j] * f.x * r * f.y;
+            }
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); // the copies below read what was written
+    tc_fence_before();
+    __syncthreads();
     cluster_wait(); // every CTA of the cluster runs
     if (a.cols > kLinLandingCols) {
         cluster_arrive();
         cluster_wait(); // and is done with its ring
     }
-    if (warp < kLinDecoders) {
-        tc_fence_after();
-        const int quarter = warp & 3, row = quarter * 32 + lane;
-        const int owner = (row * a.own_inv) >> 16; // row / own
-        uint32_t to;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(to)
-                     : "r"(smem_addr(land + split * a.cols * a.own + row - owner * a.own)), "r"(owner));
-        // The row's factor (g, or 2^E) between the two halves of the column's:
-        // neither alone need keep a sum inside fp32's range that both together
-        // leave there.
-        const float r = kNv ? s_g : e8m0_to_f32(top);
-        for (int p = 0; p < a.parts; ++p)
-            for (int c = p * groups + (warp >> 2) * 8; c < p * groups + have; c += 16) {
-                float v[8];
-                tc_load_8(tmem + (uint32_t)c + ((uint32_t)(quarter * 32) << 16), v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 f = s_factor[c + j];
-                    const float y = v[j] * f.x * r * f.y;
-                    if (c + j < p * groups + have)
-                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + (uint32_t)((c + j) * a.own * 4)), "f"(y)
-                                     : "memory");
-                }
-            }
-    }
-    tc_fence_before();
-    cluster_arrive();
-    cluster_wait();
     if (warp == kLinDecoders + 1)
         tmem_dealloc(tmem, tmem_cols);
+    if (warp == 0 && lane < splits) { // each owner its rows (whole blocks: columns without a row hold anything)
+        uint32_t dst, bar;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_addr(land + split * a.cols * a.own)), "r"(lane));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_addr(&landed)), "r"(lane));
+        asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                     "r"(smem_addr(part + lane * a.cols * a.own)), "r"(a.cols * a.own * 4), "r"(bar)
+                     : "memory");
+    }
+    __syncwarp();
 
     // ---- the rows of this CTA, summed over the cluster in order ----
+    if (!mbar_wait(&landed, 0))
+        raise_status(a.status, kStatusTimeout);
     const int col0 = band * kLinRows + split * a.own;
     const int mine = min(min(a.own, kLinRows - split * a.own), a.N - col0);
-    for (int m = warp; m < have; m += kLinThreads / 32)
-        for (int r = lane; r < mine; r += 32) {
-            float y = 0.0f;
-            for (int p = 0; p < a.parts; ++p) {
-                const float *const src = land + (p * groups + m) * a.own + r;
+    for (int i = (int)threadIdx.x; i < have * a.own; i += kLinThreads) {
+        const int m = (int)__umulhi((uint32_t)i, a.own_magic), r = i - m * a.own; // i / own
+        if (r >= mine)
+            continue;
+        float y = 0.0f;
+        for (int p = 0; p < a.parts; ++p) {
+            const float *const src = land + (p * groups + m) * a.own + r;
+            float f[kLinMaxSplits];
 #pragma unroll
-                for (int s = 0; s < kLinMaxSplits; ++s)
-                    if (s < splits)
-                        y += src[s * a.cols * a.own];
-            }
-            const int64_t o = (int64_t)(mtile * groups + m) * a.N + col0 + r;
-            if (a.out_bf16)
-                static_cast<uint16_t *>(a.y)[o] = to_out<uint16_t>(y);
-            else
-                static_cast<float *>(a.y)[o] = y;
+            for (int s = 0; s < kLinMaxSplits; ++s)
+                f[s] = s < splits ? src[s * a.cols * a.own] : 0.0f;
+#pragma unroll
+            for (int s = 0; s < kLinMaxSplits; ++s)
+                y += f[s];
         }
+        const int64_t o = (int64_t)(mtile * groups + m) * a.N + col0 + r;
+        if (a.out_bf16)
+            static_cast<uint16_t *>(a.y)[o] = to_out<uint16_t>(y);
+        else
+            static_cast<float *>(a.y)[o] = y;
+    }
+    // this CTA's shared memory is the source of copies until they have landed
+    cluster_arrive();
+    cluster_wait();
 }
 
 } // namespace fp4

@@ -562,8 +562,8 @@ fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const void *q, fp4_dtype 
  * A NaN or Inf in x sets NONFINITE (its row of y is then unspecified, the
  * others are not).  N and rows
  * below 2^23, K below 2^31 - 1024 (else FP4_ERR_SHAPE).  rows or N = 0: nothing is done;
- * K = 0: y = 0.  Reads the weight once for every 64 rows (32 for fp32 x).  Two kernels;
- * the workspace (any contents) holds the laid-out activations. */
+ * K = 0: y = 0.  Reads the weight once for every 160 rows (80 for fp32 x).  One kernel, or
+ * two where the activations are laid out first, in the workspace (any contents). */
 size_t fp4_linear_workspace_bytes(int64_t rows, int64_t K);
 fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t rows, int64_t K, int64_t x_stride,
                       const uint8_t *packed, const uint8_t *scales_mma, const float *global_scale, int64_t N, void *y,
