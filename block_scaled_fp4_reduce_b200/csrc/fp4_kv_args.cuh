@@ -43,6 +43,7 @@ inline fp4::KvCache device_cache(const fp4_kv_cache &c)
     d.g[0] = c.k_global_scale;
     d.g[1] = c.v_global_scale;
     d.slots = c.num_pages * c.page_size;
+    d.page_magic = ~(uint64_t)0 / (uint64_t)c.page_size + 1;
     d.heads = c.heads;
     d.blocks = c.head_dim / (c.format == FP4_NVFP4 ? 16 : 32);
     d.page = c.page_size;

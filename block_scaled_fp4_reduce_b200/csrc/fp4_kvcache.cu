@@ -30,14 +30,15 @@ fp4_status check_rows(const fp4_kv_cache &c, const void *k, const void *v, fp4_d
 }
 
 // Units of a row side by side in a CTA, and the grid over them: x walks the
-// tokens (at most `most` CTAs in all, each thread keeping its unit), y the
+// tokens (at most most_per_sm CTAs an SM, each thread keeping its unit), y the
 // units beyond one CTA's.
-template <typename K> fp4_status kv_grid(K kernel, int64_t units, int64_t tokens, int &per, dim3 &grid)
+template <typename K>
+fp4_status kv_grid(K kernel, int64_t units, int64_t tokens, int most_per_sm, int &per, dim3 &grid)
 {
     per = (int)(units < kThreads ? units : kThreads);
     const int64_t tiles = (units + per - 1) / per, per_cta = kThreads / per;
     const int64_t steps = (tokens + per_cta - 1) / per_cta;
-    const int most = grid_for(kernel, INT_MAX, 1);
+    const int most = grid_for(kernel, INT_MAX, 1, kThreads, 0, most_per_sm);
     if (most <= 0)
         return FP4_ERR_CUDA;
     int64_t x = most / tiles > 1 ? most / tiles : 1;
@@ -55,7 +56,7 @@ fp4_status launch_write(const fp4_kv_cache &c, const void *k, const void *v, int
     const fp4::KvCache d = fp4_kv::device_cache(c);
     int per;
     dim3 grid;
-    const fp4_status st = kv_grid(kernel, (int64_t)2 * d.heads * d.blocks, tokens, per, grid);
+    const fp4_status st = kv_grid(kernel, (int64_t)2 * d.heads * d.blocks, tokens, 0, per, grid);
     if (st != FP4_OK)
         return st;
     return launch_cfg(kernel, grid, kThreads, 0, stream, d, static_cast<const T *>(k), static_cast<const T *>(v),
@@ -70,7 +71,7 @@ fp4_status launch_read(const fp4_kv_cache &c, void *k, void *v, int64_t tokens, 
     const fp4::KvCache d = fp4_kv::device_cache(c);
     int per;
     dim3 grid;
-    const fp4_status st = kv_grid(kernel, (int64_t)2 * d.heads * (c.head_dim / 16), tokens, per, grid);
+    const fp4_status st = kv_grid(kernel, (int64_t)2 * d.heads * (c.head_dim / 16), tokens, fp4::kKvReadCtas, per, grid);
     if (st != FP4_OK)
         return st;
     return launch_cfg(kernel, grid, kThreads, 0, stream, d, static_cast<T *>(k), static_cast<T *>(v), k_stride,

@@ -10,6 +10,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "fp4_kernels.cuh"
 
@@ -19,14 +20,15 @@ namespace fp4 {
 struct KvCache {
     uint8_t *packed[2], *scales[2];
     const float *g[2];
-    int64_t slots; // num_pages * page_size
+    int64_t slots;       // num_pages * page_size
+    uint64_t page_magic; // 2^64 / page, rounded up: slots lie below 2^40
     int heads, blocks, page; // blocks of a token's head: head_dim / G
 };
 
 // Row (token of one head) of a slot.
 __device__ __forceinline__ int64_t kv_row(const KvCache &c, int64_t slot, int head)
 {
-    const int64_t page = slot / c.page;
+    const int64_t page = (int64_t)__umul64hi((uint64_t)slot, c.page_magic);
     return (page * c.heads + head) * c.page + (slot - page * c.page);
 }
 
@@ -61,64 +63,96 @@ __device__ __forceinline__ KvUnit kv_unit(const KvCache &c, int units_of_row, in
 
 // ---------------------------------------------------------------------------
 // Write.  One thread per block (32-byte loads, one packed store, one scale
-// byte), kKvTokens tokens in flight.
+// byte), kKvWriteTokens tokens in flight.  The loop is the CTA's, so that its
+// warps stay whole for the NVFP4 bf16 path, whose half-blocks next to a
+// rounding border are divided by the whole warp (nv_quantize_warp).
 // ---------------------------------------------------------------------------
-constexpr int kKvTokens = 2;
+constexpr int kKvWriteTokens = 2;
 
 template <typename T, bool kNv, bool kCeil>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kNv && sizeof(T) == 2 ? 4 : 1)
     kv_write_kernel(const KvCache c, const T *__restrict__ k, const T *__restrict__ v, int64_t k_stride,
                     int64_t v_stride, const int64_t *__restrict__ slots, int64_t tokens, int per, int32_t *status)
 {
-    constexpr int G = kNv ? 16 : 32;
+    constexpr int G = kNv ? 16 : 32, U = kKvWriteTokens;
+    constexpr bool kShared = kNv && sizeof(T) == 2;
+    struct None {};
+    using Queue = std::conditional_t<kShared, NvExactQueue<U>, None>;
+    __shared__ Queue queue[kShared ? kThreads / 32 : 1];
     pdl_begin();
-    const KvUnit u = kv_unit(c, c.blocks, per);
-    if (!u.any)
-        return;
+    KvUnit u = kv_unit(c, c.blocks, per);
     NvScaleConsts sc = {};
     if constexpr (kNv) {
-        const float g = __ldcg(c.g[u.sel] + u.head);
+        float g = u.any ? __ldcg((u.sel ? c.g[1] : c.g[0]) + u.head) : 1.0f;
         // 448 g has to be finite, and a subnormal g has no usable reciprocal
         if (!(g >= 0x1p-126f && g <= 3.4028234663852886e38f / 2688.0f)) {
             raise_status(status, kStatusRange);
-            return;
+            u.any = false;
+            g = 1.0f;
         }
         sc = nv_scale_consts(g);
     }
     const T *x = (u.sel ? v : k) + (int64_t)(u.head * c.blocks + u.block) * G;
     const int64_t stride = u.sel ? v_stride : k_stride;
-    uint8_t *const packed = c.packed[u.sel], *const scales = c.scales[u.sel];
+    // (not indexed by u.sel: that would copy the arguments to local memory)
+    uint8_t *const packed = u.sel ? c.packed[1] : c.packed[0], *const scales = u.sel ? c.scales[1] : c.scales[0];
     int32_t err = 0;
-    for (int64_t t = u.first; t < tokens; t += (int64_t)kKvTokens * u.step) {
-        Blk<T, G> blk[kKvTokens];
-        int64_t slot[kKvTokens];
+    const int64_t tok = u.first - (int64_t)blockIdx.x * (kThreads / per); // the thread's place among the CTA's tokens
+    for (int64_t t = u.first; t - tok < tokens; t += (int64_t)U * u.step) {
+        Blk<T, G> blk[U];
+        int64_t at[U];
 #pragma unroll
-        for (int i = 0; i < kKvTokens; ++i) {
+        for (int i = 0; i < U; ++i) {
             const int64_t ti = t + (int64_t)i * u.step;
-            slot[i] = -1;
-            if (ti < tokens) {
-                slot[i] = __ldcg(slots + ti);
-                if (slot[i] >= c.slots) {
-                    err = kStatusIndex;
-                    slot[i] = -1;
-                }
-                load_blk(x + ti * stride, 0, blk[i]);
+            at[i] = u.any && ti < tokens ? __ldcg(slots + ti) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (at[i] >= c.slots) {
+                err = kStatusIndex;
+                at[i] = -1;
+            }
+            if (at[i] >= 0) {
+                load_blk(x + (t + (int64_t)i * u.step) * stride, 0, blk[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < Blk<T, G>::kWords; ++j)
+                    blk[i].w[j] = 0u;
             }
         }
 #pragma unroll
-        for (int i = 0; i < kKvTokens; ++i) {
-            if (slot[i] < 0)
-                continue;
-            const int64_t at = kv_row(c, slot[i], u.head) * c.blocks + u.block;
-            if constexpr (kNv) {
+        for (int i = 0; i < U; ++i)
+            if (at[i] >= 0)
+                at[i] = kv_row(c, at[i], u.head) * c.blocks + u.block;
+        if constexpr (kShared) {
+            uint2 pk[U];
+            uint32_t code[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
                 if (absmax_bits(blk[i]) >= kNonFiniteBits)
                     err = kStatusNonFinite;
-                nv_quantize_block(blk[i], sc, reinterpret_cast<uint2 *>(packed) + at, scales + at);
-            } else {
-                bool bad = false;
-                mx_quantize_block<kCeil>(blk[i], reinterpret_cast<uint4 *>(packed) + at, scales + at, bad);
-                if (bad)
-                    err = kStatusNonFinite;
+            nv_quantize_warp<U>(blk, sc, queue[threadIdx.x >> 5], pk, code);
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (at[i] >= 0) {
+                    reinterpret_cast<uint2 *>(packed)[at[i]] = pk[i];
+                    scales[at[i]] = (uint8_t)code[i];
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (at[i] < 0)
+                    continue;
+                if constexpr (kNv) {
+                    if (absmax_bits(blk[i]) >= kNonFiniteBits)
+                        err = kStatusNonFinite;
+                    nv_quantize_block(blk[i], sc, reinterpret_cast<uint2 *>(packed) + at[i], scales + at[i]);
+                } else {
+                    bool bad = false;
+                    mx_quantize_block<kCeil>(blk[i], reinterpret_cast<uint4 *>(packed) + at[i], scales + at[i], bad);
+                    if (bad)
+                        err = kStatusNonFinite;
+                }
             }
         }
     }
@@ -128,8 +162,11 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---------------------------------------------------------------------------
 // Read back.  One thread per 16 codes (8 packed bytes, one scale byte, 16
-// outputs), as the dequantiser.
+// outputs), as the dequantiser; kKvTokens tokens in flight,
+// kKvReadCtas CTAs per SM.
 // ---------------------------------------------------------------------------
+constexpr int kKvTokens = 2, kKvReadCtas = 8;
+
 template <typename T, bool kNv>
 __global__ void __launch_bounds__(kThreads)
     kv_read_kernel(const KvCache c, T *__restrict__ k, T *__restrict__ v, int64_t k_stride, int64_t v_stride,
@@ -140,32 +177,36 @@ __global__ void __launch_bounds__(kThreads)
     const KvUnit u = kv_unit(c, units, per);
     if (!u.any)
         return;
-    const float g = kNv ? __ldcg(c.g[u.sel] + u.head) : 1.0f;
+    const float g = kNv ? __ldcg((u.sel ? c.g[1] : c.g[0]) + u.head) : 1.0f;
     const uint64_t g2 = pack2(g, g);
     T *y = (u.sel ? v : k) + (int64_t)(u.head * units + u.block) * 16;
     const int64_t stride = u.sel ? v_stride : k_stride;
-    const uint2 *const packed = reinterpret_cast<const uint2 *>(c.packed[u.sel]);
-    const uint8_t *const scales = c.scales[u.sel];
+    const uint2 *const packed = reinterpret_cast<const uint2 *>(u.sel ? c.packed[1] : c.packed[0]);
+    const uint8_t *const scales = u.sel ? c.scales[1] : c.scales[0];
     bool bad = false;
+    auto slot_of = [&](int64_t ti) -> int64_t { return ti < tokens ? __ldcg(slots + ti) : -1; };
+    int64_t next[kKvTokens]; // slots are read a round ahead
+#pragma unroll
+    for (int i = 0; i < kKvTokens; ++i)
+        next[i] = slot_of(u.first + (int64_t)i * u.step);
     for (int64_t t = u.first; t < tokens; t += (int64_t)kKvTokens * u.step) {
         uint2 pk[kKvTokens];
         uint32_t sbyte[kKvTokens];
 #pragma unroll
         for (int i = 0; i < kKvTokens; ++i) {
-            const int64_t ti = t + (int64_t)i * u.step;
             pk[i] = make_uint2(0u, 0u); // zeros where there is nothing to read
             sbyte[i] = kNv ? 0u : 127u;
-            if (ti < tokens) {
-                const int64_t slot = __ldcg(slots + ti);
-                if (slot >= c.slots) {
-                    bad = true;
-                } else if (slot >= 0) {
-                    const int64_t at = kv_row(c, slot, u.head) * units + u.block;
-                    pk[i] = __ldcg(packed + at);
-                    sbyte[i] = __ldcg(scales + (kNv ? at : at >> 1));
-                }
+            if (next[i] >= c.slots) {
+                bad = true;
+            } else if (next[i] >= 0) {
+                const int64_t at = kv_row(c, next[i], u.head) * units + u.block;
+                pk[i] = __ldcg(packed + at);
+                sbyte[i] = __ldcg(scales + (kNv ? at : at >> 1));
             }
         }
+#pragma unroll
+        for (int i = 0; i < kKvTokens; ++i)
+            next[i] = slot_of(t + (int64_t)(kKvTokens + i) * u.step);
 #pragma unroll
         for (int i = 0; i < kKvTokens; ++i) {
             const int64_t ti = t + (int64_t)i * u.step;
