@@ -712,11 +712,11 @@ def kv_read(cache: KVCache, slots: torch.Tensor, out_dtype=torch.bfloat16, k=Non
 
 
 def kv_attention_workspace(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor) -> torch.Tensor:
-    """A workspace for every kv_attention call on this cache that gets it, on
-    one stream at a time."""
+    """A (zero-filled) workspace for kv_attention calls of this shape, or of
+    smaller batches, on caches of this head_dim, on one stream at a time."""
     B, L, HQ, _ = q.shape
     n = lib().fp4_kv_attention_workspace_bytes(cache._ref, B, L, HQ, page_table.shape[1])
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=cache.device)
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, scale=None,

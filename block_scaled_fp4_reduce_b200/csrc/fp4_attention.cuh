@@ -4,7 +4,7 @@
 //
 // The query rows that read one KV head (new tokens x query heads of the
 // group) form a tile of 8 NT rows.  Grid: one CTA per (sequence, KV head, row
-// tile, split of the tokens); its kAttnWarps warps take steps of 32 tokens in
+// tile), or an even share of all of them (attn_share); its kAttnWarps warps take steps of 32 tokens in
 // turn, each warp on its own -- own ring of staged steps (cp.async, kStages
 // deep), own running maximum, sum and output -- and meet once, at the end.
 // One pass over the cache; scores live in registers.
@@ -56,7 +56,8 @@ struct AttnArgs {
     KvCache c;
     const void *q;
     int batch, q_tokens, q_heads;
-    int group, rows, row_tiles, splits, chunk; // rows = q_tokens * group; chunk: tokens of a split
+    int group, rows, row_tiles; // rows = q_tokens * group
+    int split;                  // 0: a CTA per unit; 1: the tokens are shared out evenly (attn_share)
     int64_t q_stride;
     const int32_t *page_table;
     int table_width;
@@ -66,14 +67,17 @@ struct AttnArgs {
     float scale; // softmax scale * log2(e)
     void *out;
     float *lse;
-    float *partial;  // [unit][split][8 NT][D] outputs of a split, unnormalised
-    float4 *stats;   // [unit][split][8 NT] m, l, m'
+    float *partial;  // [2 CTAs][8 NT][D] outputs of a piece of a unit, unnormalised
+    float4 *stats;   // [2 CTAs][8 NT] m, l, m'
+    uint32_t *arrived; // [unit] pieces of it that are done; zero between calls
     int32_t *status;
 };
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnStep = 32;       // tokens of a warp's step
+constexpr int kAttnRound = kAttnWarps * kAttnStep; // of a step of all warps
+constexpr int kAttnMinShare = 2;    // rounds: a CTA's start and end cost about as much as two
 // Weights enter the tensor cores times 2^kAttnBias, and pass the reference
 // by at most 2^kAttnSlack: 2^15 is the largest power of two in fp16.
 constexpr float kAttnBias = 11.0f, kAttnSlack = 4.0f;
@@ -94,6 +98,27 @@ template <bool kNv, int D, int NT> constexpr int attn_smem()
     const int ring = kAttnWarps * kAttnStages<D> * kAttnStageBytes<kNv, D>;
     const int merge = kAttnWarps * 8 * NT * (D + 4) * 4;
     return ring > merge ? ring : merge;
+}
+
+// N 32-bit words, whole vectors (the address aligned to them).
+template <typename T, int N> __device__ __forceinline__ void load_words(const T *p, uint32_t (&w)[N])
+{
+    if constexpr (N == 1) {
+        w[0] = __ldcg(reinterpret_cast<const uint32_t *>(p));
+    } else if constexpr (N == 2) {
+        const uint2 v = __ldcg(reinterpret_cast<const uint2 *>(p));
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(p) + i / 4);
+            w[i] = v.x;
+            w[i + 1] = v.y;
+            w[i + 2] = v.z;
+            w[i + 3] = v.w;
+        }
+    }
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -121,27 +146,31 @@ __device__ __forceinline__ uint32_t max_byte(uint32_t v)
     return max(a, b);
 }
 
-// Positions that a row tile needs, and its splits: tokens [lo, hi], staged
-// from `base` (lo rounded down to 16) in `ns` splits of `chunk` tokens.
+// Positions that a row tile needs: tokens [lo, hi] (none where hi < lo), staged
+// from `base` (lo rounded down to 16) in rounds of kAttnRound tokens.
 struct AttnSpan {
-    int n, lo, hi, base, ns;
+    int n, lo, hi, base;
 };
 
-__device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int b, int first_token, int last_token)
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int n, int first_token, int last_token)
 {
     AttnSpan s;
-    s.n = __ldcg(a.seq_lens + b);
-    if (s.n < 0 || s.n > a.capacity) {
-        raise_status(a.status, kStatusIndex);
-        s.n = 0;
-    }
-    s.hi = s.n - a.q_tokens + last_token; // may be negative: nothing to see
+    s.n = n < 0 || n > a.capacity ? 0 : n; // (reported by the caller)
+    s.hi = s.n - a.q_tokens + last_token;  // may be negative: nothing to see
     const int p = s.n - a.q_tokens + first_token;
     s.lo = a.window > 0 && p >= a.window ? p - (int)a.window + 1 : 0;
     s.base = s.lo & ~15;
-    s.ns = s.hi < s.lo ? 0 : (s.hi - s.base) / a.chunk + 1;
     return s;
 }
+
+// Rounds of a unit, one at least (a unit that sees nothing is written too).
+__device__ __forceinline__ int attn_rounds(const AttnSpan &s)
+{
+    return s.hi < s.lo ? 1 : (s.hi - s.base) / kAttnRound + 1;
+}
+
+// New token of row r of a KV head's rows.
+__device__ __forceinline__ int attn_token(const AttnArgs &a, int r) { return a.q_tokens == 1 ? 0 : r / a.group; }
 
 // What turns a row's summed output into its result: g / l, and for MXFP4
 // 2^(m' - m), in two factors because the power alone may leave fp32's range.
@@ -171,6 +200,253 @@ __device__ __forceinline__ float attn_lse(float m, float l)
     return l > 0.0f ? (m + (log2f(l) - kAttnBias)) * kLn2 : -INFINITY;
 }
 
+// Four elements of a row's result, from d on, and with the first its lse.
+template <typename TQ, bool kNv, int D>
+__device__ __forceinline__ void attn_write(const AttnArgs &a, int b, int kvh, int row, int d, float4 v, float m, float l,
+                                           float mw)
+{
+    const int i = attn_token(a, row);
+    const int64_t at = ((int64_t)b * a.q_tokens + i) * a.q_heads + kvh * a.group + row - i * a.group;
+    const AttnScale f = attn_scale<kNv>(a, kvh, m, mw, l);
+    TQ *const dst = static_cast<TQ *>(a.out) + at * D + d;
+    const float y[4] = {v.x * f.f * f.f2, v.y * f.f * f.f2, v.z * f.f * f.f2, v.w * f.f * f.f2};
+    if constexpr (sizeof(TQ) == 2) {
+        uint2 w;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(y[1]), "f"(y[0]));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(y[3]), "f"(y[2]));
+        *reinterpret_cast<uint2 *>(dst) = w;
+    } else {
+        *reinterpret_cast<float4 *>(dst) = make_float4(y[0], y[1], y[2], y[3]);
+    }
+    if (a.lse && d == 0)
+        a.lse[at] = attn_lse(m, l);
+}
+
+// ---------------------------------------------------------------------------
+// How the tokens are shared out.  A unit is one sequence, row tile and KV head;
+// its work is its rounds.  With the units in that order (heads innermost) and
+// all rounds numbered through, CTA i takes rounds [i s, (i + 1) s), s = the
+// total over the CTAs that fit on the GPU: every CTA has the same work whatever
+// the lengths are, in one wave.  The lengths are on the device, so every CTA
+// forms the numbering for itself, a scan over the sequences.  A CTA whose
+// rounds cross units takes them one after the other; a unit that crosses CTAs
+// leaves pieces, which the CTA that finishes the last of them joins.
+// ---------------------------------------------------------------------------
+template <int R> __device__ __forceinline__ uint32_t attn_sequence_rounds(const AttnArgs &a, int len)
+{
+    uint32_t sum = 0;
+    for (int rt = 0; rt < a.row_tiles; ++rt) {
+        const int row0 = rt * R, rows = min(R, a.rows - row0);
+        sum += (uint32_t)attn_rounds(attn_span(a, len, attn_token(a, row0), attn_token(a, row0 + rows - 1)));
+    }
+    return sum * (uint32_t)a.c.heads;
+}
+
+// Inclusive scan of one value a thread over the CTA's kAttnThreads threads;
+// `total` receives the sum.
+__device__ __forceinline__ uint32_t attn_scan(uint32_t v, uint32_t *s_warp, uint32_t &total)
+{
+    const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d)
+            v += o;
+    }
+    __syncthreads();
+    if (lane == 31)
+        s_warp[warp] = v;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+        if (w < warp)
+            v += s_warp[w];
+        total += s_warp[w];
+    }
+    return v;
+}
+
+// This CTA's share: the sequence its first round lies in, that round's number
+// within the sequence, the rounds from there on, and the CTAs' common share;
+// false if there are none.  (The host sees to it that all rounds number below
+// 2^31.)
+struct AttnShare {
+    int b, len; // len: of sequence b
+    uint32_t at, left, each, done; // done: rounds this CTA has behind it
+};
+
+template <int R> __device__ __forceinline__ bool attn_share(const AttnArgs &a, AttnShare &out)
+{
+    __shared__ uint32_t s_warp[kAttnWarps], s_at;
+    __shared__ int s_b;
+    const int tid = (int)threadIdx.x;
+    uint32_t all = 0, mine = 0, upto = 0, total;
+    if (a.batch <= 32) { // every warp finds it for itself
+        const int lane = tid & 31;
+        int len = 0;
+        if (lane < a.batch) {
+            len = __ldcg(a.seq_lens + lane);
+            if ((len < 0 || len > a.capacity) && blockIdx.x == 0)
+                raise_status(a.status, kStatusIndex);
+            mine = attn_sequence_rounds<R>(a, len);
+        }
+        upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d)
+                upto += o;
+        }
+        all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        const uint32_t each = max((all + gridDim.x - 1) / gridDim.x, (uint32_t)kAttnMinShare);
+        const uint32_t first = each * blockIdx.x;
+        if (first >= all)
+            return false;
+        out.b = __ffs(__ballot_sync(0xFFFFFFFFu, first < upto)) - 1;
+        out.at = first - __shfl_sync(0xFFFFFFFFu, upto - mine, out.b);
+        out.len = __shfl_sync(0xFFFFFFFFu, len, out.b);
+        out.left = min(each, all - first);
+        out.each = each;
+        out.done = 0;
+        return true;
+    }
+    for (int b0 = 0; b0 < a.batch; b0 += kAttnThreads) {
+        mine = 0;
+        if (b0 + tid < a.batch) {
+            const int len = __ldcg(a.seq_lens + b0 + tid);
+            if ((len < 0 || len > a.capacity) && blockIdx.x == 0)
+                raise_status(a.status, kStatusIndex);
+            mine = attn_sequence_rounds<R>(a, len);
+        }
+        upto = attn_scan(mine, s_warp, total);
+        all += total;
+    }
+    const uint32_t each = max((all + gridDim.x - 1) / gridDim.x, (uint32_t)kAttnMinShare);
+    const uint32_t first = each * blockIdx.x; // below 2^32: each <= all / grid + kAttnMinShare
+    if (first >= all)
+        return false;
+    uint32_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kAttnThreads) {
+        if (a.batch > kAttnThreads) { // otherwise the one scan above holds
+            mine = b0 + tid < a.batch ? attn_sequence_rounds<R>(a, __ldcg(a.seq_lens + b0 + tid)) : 0;
+            upto = attn_scan(mine, s_warp, total);
+        }
+        if (first >= before + upto - mine && first < before + upto) {
+            s_b = b0 + tid;
+            s_at = first - (before + upto - mine);
+        }
+        before += total;
+        if (first < before)
+            break;
+    }
+    __syncthreads();
+    out.b = s_b;
+    out.len = __ldcg(a.seq_lens + s_b);
+    out.at = s_at;
+    out.left = min(each, all - first);
+    out.each = each;
+    out.done = 0;
+    return true;
+}
+
+// ---------------------------------------------------------------------------
+// The pieces of a unit, merged by the CTA that finishes the last of them:
+// pieces first .. first + count - 1 are CTAs, the second of whose two lines is
+// the first CTA's (its rounds end with the unit's beginning).  The sum runs in
+// the order of the pieces, whoever forms it.
+// ---------------------------------------------------------------------------
+constexpr int kAttnMerge = 128; // pieces whose factors are held at a time
+
+template <typename TQ, bool kNv, int D, int R>
+__device__ __forceinline__ void attn_merge(const AttnArgs &a, uint8_t *smem, int b, int kvh, int row0, int rows, int first,
+                                           int count)
+{
+    float(*const factor)[kAttnMerge] = reinterpret_cast<float(*)[kAttnMerge]>(smem); // [row][piece]
+    float(*const top)[4] = reinterpret_cast<float(*)[4]>(smem + R * kAttnMerge * 4); // [row] m, l, m'
+    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+    auto line = [&](int s, int r) -> int64_t { return (int64_t)(2 * (first + s) + (s == 0)) * R + r; };
+    // A warp takes rows warp, warp + 4, ...; a lane holds one piece's statistics
+    // of each (more than 32 pieces: the others are read again where they are needed).
+    constexpr int kMine = R / kAttnWarps;
+    float4 own[kMine];
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        own[j] = make_float4(-kAttnNone, 0.0f, -kAttnNone, 0.0f);
+        if (warp + j * kAttnWarps < rows && lane < count)
+            own[j] = __ldcg(a.stats + line(lane, warp + j * kAttnWarps));
+    }
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const int r = warp + j * kAttnWarps;
+        if (r >= rows)
+            break;
+        float mm = own[j].x, mx = own[j].z;
+        for (int s = lane + 32; s < count; s += 32) {
+            const float4 st = __ldcg(a.stats + line(s, r));
+            mm = fmaxf(mm, st.x);
+            mx = fmaxf(mx, st.z);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, d));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+        }
+        float ll = own[j].y * ex2(own[j].x - mm);
+        for (int s = lane + 32; s < count; s += 32) {
+            const float4 st = __ldcg(a.stats + line(s, r));
+            ll = fmaf(st.y, ex2(st.x - mm), ll);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            ll += __shfl_xor_sync(0xFFFFFFFFu, ll, d);
+        if (lane == 0) {
+            top[r][0] = mm;
+            top[r][1] = ll;
+            top[r][2] = mx;
+        }
+        if (lane < count)
+            factor[r][lane] = ex2(own[j].z - mx);
+        for (int s = lane + 32; s < min(count, kAttnMerge); s += 32)
+            factor[r][s] = ex2(__ldcg(a.stats + line(s, r)).z - mx);
+    }
+    constexpr int kItems = R * D / 4 / kAttnThreads; // of four elements, of a thread
+    float4 v[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+        v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s0 = 0; s0 < count; s0 += kAttnMerge) {
+        const int n = min(kAttnMerge, count - s0);
+        __syncthreads();
+        if (s0 > 0) {
+            for (int r = warp; r < rows; r += kAttnWarps)
+                for (int s = lane; s < n; s += 32)
+                    factor[r][s] = ex2(__ldcg(a.stats + line(s0 + s, r)).z - top[r][2]);
+            __syncthreads();
+        }
+#pragma unroll 8
+        for (int s = 0; s < n; ++s)
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int idx = (int)threadIdx.x + i * kAttnThreads, r = idx / (D / 4), d = idx % (D / 4) * 4;
+                if (r < rows) {
+                    const float4 p = __ldcg(reinterpret_cast<const float4 *>(a.partial + line(s0 + s, r) * D + d));
+                    const float f = factor[r][s];
+                    v[i].x = fmaf(p.x, f, v[i].x);
+                    v[i].y = fmaf(p.y, f, v[i].y);
+                    v[i].z = fmaf(p.z, f, v[i].z);
+                    v[i].w = fmaf(p.w, f, v[i].w);
+                }
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int idx = (int)threadIdx.x + i * kAttnThreads, r = idx / (D / 4), d = idx % (D / 4) * 4;
+        if (r < rows)
+            attn_write<TQ, kNv, D>(a, b, kvh, row0 + r, d, v[i], top[r][0], top[r][1], top[r][2]);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // TQ: uint16_t (bf16) or float.
 // ---------------------------------------------------------------------------
@@ -187,25 +463,75 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
     __shared__ float s_exp[R]; // 2^(exponent taken out of the row)
 
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int unit = (int)blockIdx.x / a.splits, split = (int)blockIdx.x - unit * a.splits;
-    const int bh = unit / a.row_tiles, rt = unit - bh * a.row_tiles;
-    const int b = bh / a.c.heads, kvh = bh - b * a.c.heads;
-    const int row0 = rt * R, rows = min(R, a.rows - row0);
-    const int i0 = row0 / a.group; // new token of the first row
     pdl_begin();
-    const AttnSpan sp = attn_span(a, b, i0, (row0 + rows - 1) / a.group);
-    if (split > 0 && split >= sp.ns)
+    AttnShare share = {(int)blockIdx.z, 0, 0, 1, 0, 0};
+    if (a.split && !attn_share<R>(a, share))
         return;
+    const int64_t pages = a.c.slots / a.c.page;
+    do { // one unit, or a piece of one
+    const int b = share.b;
+    int kvh = (int)blockIdx.y, rt = 0, len;
+    if (a.split) {
+        len = share.len;
+    } else {
+        if (a.row_tiles > 1) {
+            kvh = (int)blockIdx.y / a.row_tiles;
+            rt = (int)blockIdx.y - kvh * a.row_tiles;
+        }
+        len = 0; // read below, after the query rows are asked for
+    }
+    int from = 0, to = 0, all_rounds = 0; // rounds of the unit
+    if (a.split) {
+        uint32_t at = share.at;
+        for (;; ++rt) {
+            const AttnSpan s = attn_span(a, len, attn_token(a, rt * R), attn_token(a, min(rt * R + R, a.rows) - 1));
+            all_rounds = attn_rounds(s);
+            if (at < (uint32_t)all_rounds * a.c.heads)
+                break;
+            at -= (uint32_t)all_rounds * a.c.heads;
+        }
+        kvh = (int)(at / (uint32_t)all_rounds);
+        from = (int)at - kvh * all_rounds;
+        to = (int)min((uint32_t)all_rounds, from + share.left);
+    }
+    const int row0 = rt * R, rows = min(R, a.rows - row0);
+    const int i0 = attn_token(a, row0); // new token of the first row
+    // What the start needs from memory is asked for at once: the length, the
+    // query rows (a warp takes rows warp, warp + 4, ...; a lane D / 32
+    // neighbouring elements) and, below, the page table.
+    if (!a.split)
+        len = __ldcg(a.seq_lens + b);
+    constexpr int kQRows = R / kAttnWarps, kPerLane = D / 32;
+    uint32_t qraw[kQRows][kPerLane * (int)sizeof(TQ) / 4];
+#pragma unroll
+    for (int j = 0; j < kQRows; ++j) {
+        const int r = warp + j * kAttnWarps;
+        if (r < rows) {
+            const int i = attn_token(a, row0 + r), h = kvh * a.group + (row0 + r) - i * a.group;
+            load_words(static_cast<const TQ *>(a.q) + ((int64_t)b * a.q_tokens + i) * a.q_stride + (int64_t)h * D +
+                           lane * kPerLane,
+                       qraw[j]);
+        } else {
+#pragma unroll
+            for (uint32_t &w : qraw[j])
+                w = 0u;
+        }
+    }
+    const float gk = kNv ? __ldcg(a.c.g[0] + kvh) : 1.0f;
+    if (!a.split && (len < 0 || len > a.capacity))
+        raise_status(a.status, kStatusIndex);
+    const AttnSpan sp = attn_span(a, len, i0, attn_token(a, row0 + rows - 1));
+    if (!a.split)
+        to = all_rounds = attn_rounds(sp);
 
     // this warp's steps: token tok0 + 32 (warp + 4 s), below `end`
-    const int tok0 = sp.base + split * a.chunk;
-    const int end = sp.ns == 0 ? tok0 : min(sp.hi + 1, tok0 + a.chunk);
+    const int tok0 = sp.base + from * kAttnRound;
+    const int end = sp.hi < sp.lo ? tok0 : min(sp.hi + 1, sp.base + to * kAttnRound);
     const int steps_all = (end - tok0 + kAttnStep - 1) / kAttnStep;
     const int steps = steps_all > warp ? (steps_all - warp + kAttnWarps - 1) / kAttnWarps : 0;
     uint8_t *const ring = smem + warp * kStages * kStage;
     const int32_t *const table = a.page_table + (int64_t)b * a.table_width;
     const int page16 = a.c.page >> 4;
-    const int64_t pages = a.c.slots / a.c.page;
 
     // Row (in tokens of this head) of the cache that holds the 16-token
     // granule `gr` of the sequence, -1 when no token of it is needed.
@@ -288,47 +614,45 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
         cp_async_commit();
     }
 
-    // Query rows to fp16: a warp takes rows warp, warp + 4, ..., and stages
-    // them in the last stage of its ring, which the copies above left free.
+    // Query rows to fp16, staged in the last stage of each warp's ring, which
+    // the copies above left free.
     constexpr int kQRow = D + 8;
-    static_assert(kParts * 2 * NT * kQRow * 2 <= kStage, "the staged query rows");
+    static_assert(kParts * kQRows * kQRow * 2 <= kStage, "the staged query rows");
     auto q_at = [&](int p, int r) -> uint16_t * {
         uint8_t *const st = smem + ((r % kAttnWarps) * kStages + kStages - 1) * kStage;
-        return reinterpret_cast<uint16_t *>(st) + (p * (R / kAttnWarps) + r / kAttnWarps) * kQRow;
+        return reinterpret_cast<uint16_t *>(st) + (p * kQRows + r / kAttnWarps) * kQRow;
     };
-    for (int r = warp; r < R; r += kAttnWarps) {
-        float v[D / 32];
-        uint32_t top = 0;
-        const int i = (row0 + r) / a.group, h = kvh * a.group + (row0 + r) - i * a.group;
-        const TQ *q = static_cast<const TQ *>(a.q) + ((int64_t)b * a.q_tokens + i) * a.q_stride + (int64_t)h * D;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            v[e] = 0.0f;
-            if (r < rows) {
-                if constexpr (sizeof(TQ) == 2)
-                    v[e] = __uint_as_float((uint32_t)__ldcg(q + e * 32 + lane) << 16);
-                else
-                    v[e] = __ldcg(q + e * 32 + lane);
-            }
+    for (int j = 0; j < kQRows; ++j) {
+        const int r = warp + j * kAttnWarps;
+        float v[kPerLane];
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < kPerLane; ++e) {
+            if constexpr (sizeof(TQ) == 2)
+                v[e] = __uint_as_float(e & 1 ? qraw[j][e / 2] & 0xFFFF0000u : qraw[j][e / 2] << 16);
+            else
+                v[e] = __uint_as_float(qraw[j][e]);
             top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
         }
         top = __reduce_max_sync(0xFFFFFFFFu, top);
         if (top >= kNonFiniteBits && lane == 0)
             raise_status(a.status, kStatusNonFinite);
-        // times 2^(14 - floor(log2 max)), in two exact steps; rows below 2^-112 count as if their maximum were that
+        // times 2^(14 - floor(log2 max)); rows below 2^-112 count as if their maximum were that
         int ex = max((int)(top >> 23), 15) - 127; // floor(log2 max)
         if (top >= kNonFiniteBits)
             ex = 14;
         const float up = __uint_as_float((uint32_t)(127 + (14 - ex)) << 23);
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            const float x = v[e] * up;
-            const uint32_t hi = pack_f16x2(x, 0.0f) & 0xFFFFu;
-            q_at(0, r)[e * 32 + lane] = (uint16_t)hi;
+        for (int e = 0; e < kPerLane; e += 2) {
+            const float x0 = v[e] * up, x1 = v[e + 1] * up;
+            const uint32_t hi = pack_f16x2(x0, x1);
+            *reinterpret_cast<uint32_t *>(q_at(0, r) + lane * kPerLane + e) = hi;
             if constexpr (kParts == 2) {
-                float back, none;
-                f16x2_to_f32(hi, back, none);
-                q_at(1, r)[e * 32 + lane] = (uint16_t)(pack_f16x2((x - back) * 2048.0f, 0.0f) & 0xFFFFu);
+                float b0, b1;
+                f16x2_to_f32(hi, b0, b1);
+                *reinterpret_cast<uint32_t *>(q_at(1, r) + lane * kPerLane + e) =
+                    pack_f16x2((x0 - b0) * 2048.0f, (x1 - b1) * 2048.0f);
             }
         }
         if (lane == 0)
@@ -339,7 +663,6 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
     uint32_t qb[kParts][NT][KS][2];
     float rowc[NT][2];     // score of rows 2t, 2t + 1 in units of log2
     int last[NT][2], first[NT][2]; // their visible positions
-    const float gk = kNv ? __ldcg(a.c.g[0] + kvh) : 1.0f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -354,7 +677,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
         for (int e = 0; e < 2; ++e) {
             const int r = n * 8 + 2 * t + e;
             rowc[n][e] = a.scale * gk * s_exp[r];
-            last[n][e] = r < rows ? sp.n - a.q_tokens + (row0 + r) / a.group : -1;
+            last[n][e] = r < rows ? sp.n - a.q_tokens + attn_token(a, row0 + r) : -1;
             first[n][e] = a.window > 0 ? last[n][e] - (int)min(a.window, (int64_t)0x40000000) + 1 : 0;
         }
     }
@@ -377,7 +700,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
     __syncthreads(); // the staged rows are read: their stages may be filled
 
     // every row of the tile sees all of [all_lo, all_hi]
-    const int all_lo = a.window > 0 ? max(0, sp.n - a.q_tokens + (row0 + rows - 1) / a.group - (int)min(a.window, (int64_t)0x40000000) + 1) : 0;
+    const int all_lo = a.window > 0 ? max(0, sp.hi - (int)min(a.window, (int64_t)0x40000000) + 1) : 0;
     const int all_hi = sp.n - a.q_tokens + i0;
 
     uint32_t v_at[2]; // the lane's codes of the values of tokens 2t and 2t + 1
@@ -429,7 +752,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
                         acc[p][n][e] = 0.0f;
             float tokf[2]; // MXFP4: 2^E of tokens g, g + 8
             constexpr int W = D / 32; // 32-bit words of a lane's codes of a token
-            uint32_t w[2][W], sc[2][D / 64]; // scale of each 16 elements, as an f16 pair
+            uint32_t w[2][W], sc[2][D / 64]; // NVFP4: the blocks' scales in pairs; MXFP4: each 16 elements' scale twice
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int r = mt * 16 + u * 8 + g;
@@ -450,15 +773,13 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
                 }
                 if constexpr (kNv) {
                     if constexpr (D == 64) {
-                        const uint32_t f = e4m3x2_to_f16x2(ks[r * NB + t]);
-                        sc[u][0] = __byte_perm(f, f, 0x1010);
+                        sc[u][0] = e4m3x2_to_f16x2(ks[r * NB + t]); // its low half
                     } else {
 #pragma unroll
                         for (int c = 0; c < D / 128; ++c) {
                             const uint32_t f = e4m3x2_to_f16x2(
                                 *reinterpret_cast<const uint16_t *>(ks + r * NB + t * (D / 64) + 2 * c));
-                            sc[u][2 * c] = __byte_perm(f, f, 0x1010);
-                            sc[u][2 * c + 1] = __byte_perm(f, f, 0x3232);
+                            sc[u][c] = f; // the scales of two blocks
                         }
                     }
                     tokf[u] = 1.0f;
@@ -491,7 +812,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
                     e2m1_word(w[u][wd], f[u]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        f[u][j] = f16x2_mul(f[u][j], sc[u][wd / 2]);
+                        f[u][j] = kNv ? f16x2_mul_half(f[u][j], sc[u][wd / 4], wd & 2) : f16x2_mul(f[u][j], sc[u][wd / 2]);
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
@@ -748,7 +1069,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
             }
         }
     __syncthreads();
-    const bool whole = sp.ns <= 1;
+    const bool whole = to - from == all_rounds;
+    const int piece = 2 * (int)blockIdx.x + (from == 0); // a CTA's first unit may have begun before it, its last may go on
     for (int idx = (int)threadIdx.x; idx < rows * (D / 4); idx += kAttnThreads) {
         const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
         float mm = -kAttnNone, mx = -kAttnNone, ll = 0.0f;
@@ -772,124 +1094,46 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
             }
         }
         if (whole) {
-            const int i = (row0 + r) / a.group;
-            const int64_t at = ((int64_t)b * a.q_tokens + i) * a.q_heads + kvh * a.group + (row0 + r) - i * a.group;
-            const AttnScale f = attn_scale<kNv>(a, kvh, mm, mx, ll);
-            TQ *dst = static_cast<TQ *>(a.out) + at * D + d;
-            const float y[4] = {v.x * f.f * f.f2, v.y * f.f * f.f2, v.z * f.f * f.f2, v.w * f.f * f.f2};
-            if constexpr (sizeof(TQ) == 2) {
-                uint2 w2;
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w2.x) : "f"(y[1]), "f"(y[0]));
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w2.y) : "f"(y[3]), "f"(y[2]));
-                *reinterpret_cast<uint2 *>(dst) = w2;
-            } else {
-                *reinterpret_cast<float4 *>(dst) = make_float4(y[0], y[1], y[2], y[3]);
-            }
-            if (a.lse && d == 0)
-                a.lse[at] = attn_lse(mm, ll);
+            attn_write<TQ, kNv, D>(a, b, kvh, row0 + r, d, v, mm, ll, mx);
         } else {
-            const int64_t base = ((int64_t)blockIdx.x * R + r);
+            const int64_t base = (int64_t)piece * R + r;
             *reinterpret_cast<float4 *>(a.partial + base * D + d) = v;
             if (d == 0)
                 a.stats[base] = make_float4(mm, ll, mx, 0.0f);
         }
     }
-}
-
-// ---------------------------------------------------------------------------
-// The splits' results, merged: one CTA per query row.  Its warps take every
-// fourth split, a lane D / 32 neighbouring elements, and meet in shared
-// memory, always in the same order.
-// ---------------------------------------------------------------------------
-template <typename TQ, bool kNv, int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads) kv_attention_merge_kernel(const AttnArgs a)
-{
-    constexpr int R = 8 * NT, E = D / 32;
-    __shared__ float s_top[2][kAttnWarps], s_sum[kAttnWarps], s_v[kAttnWarps][D];
-    pdl_begin();
-    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
-    const int bh = (int)blockIdx.x / a.rows, r = (int)blockIdx.x - bh * a.rows;
-    const int b = bh / a.c.heads, kvh = bh - b * a.c.heads, rt = r / R, row0 = rt * R;
-    const int rows = min(R, a.rows - row0);
-    const AttnSpan sp = attn_span(a, b, row0 / a.group, (row0 + rows - 1) / a.group);
-    if (sp.ns <= 1)
-        return; // written whole
-    const int64_t base = ((int64_t)bh * a.row_tiles + rt) * a.splits;
-    const float4 *const stats = a.stats + base * R + (r - row0);
-    const float *const part = a.partial + (base * R + (r - row0)) * D + lane * E;
-    float mm = -kAttnNone, mx = -kAttnNone;
-    for (int s = (int)threadIdx.x; s < sp.ns; s += kAttnThreads) {
-        const float4 st = __ldcg(stats + (int64_t)s * R);
-        mm = fmaxf(mm, st.x);
-        mx = fmaxf(mx, st.z);
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, d));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-    }
-    if (lane == 0) {
-        s_top[0][warp] = mm;
-        s_top[1][warp] = mx;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-        mm = fmaxf(mm, s_top[0][w]);
-        mx = fmaxf(mx, s_top[1][w]);
-    }
-    float v[E], ll = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        v[e] = 0.0f;
-#pragma unroll 8
-    for (int s = warp; s < sp.ns; s += kAttnWarps) {
-        const float4 st = __ldcg(stats + (int64_t)s * R);
-        const float *p = part + (int64_t)s * R * D;
-        float w[E];
-        if constexpr (E == 2) {
-            const float2 p2 = __ldcg(reinterpret_cast<const float2 *>(p));
-            w[0] = p2.x;
-            w[1] = p2.y;
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; e += 4) {
-                const float4 p4 = __ldcg(reinterpret_cast<const float4 *>(p + e));
-                w[e] = p4.x;
-                w[e + 1] = p4.y;
-                w[e + 2] = p4.z;
-                w[e + 3] = p4.w;
+    if (a.split) {
+        if (!whole) {
+            // the unit's first round's number among all, and the CTAs that have pieces of it
+            const uint32_t u0 = share.each * blockIdx.x + share.done - (uint32_t)from;
+            const uint32_t first = u0 / share.each, last_cta = (u0 + (uint32_t)all_rounds - 1) / share.each;
+            __shared__ bool s_last;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                uint32_t *const n = a.arrived + ((int64_t)b * a.row_tiles + rt) * a.c.heads + kvh;
+                uint32_t before; // releases what this CTA wrote, acquires what the others did
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(n) : "memory");
+                s_last = before == last_cta - first;
+                if (s_last)
+                    *n = 0u;
             }
+            __syncthreads();
+            if (s_last)
+                attn_merge<TQ, kNv, D, R>(a, smem, b, kvh, row0, rows, (int)first, (int)(last_cta - first) + 1);
         }
-        const float f = ex2(st.z - mx);
-        ll = fmaf(st.y, ex2(st.x - mm), ll);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            v[e] = fmaf(w[e], f, v[e]);
+        share.left -= to - from;
+        share.at += to - from;
+        share.done += to - from;
+        if (kvh == a.c.heads - 1 && rt == a.row_tiles - 1 && to == all_rounds) {
+            share.at = 0;
+            if (++share.b < a.batch)
+                share.len = __ldcg(a.seq_lens + share.b);
+        }
+        __syncthreads(); // the merged results are read: the rings may be filled again
+    } else {
+        share.left = 0;
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        s_v[warp][lane * E + e] = v[e];
-    if (lane == 0)
-        s_sum[warp] = ll;
-    __syncthreads();
-    ll = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w)
-        ll += s_sum[w];
-    const int i = r / a.group;
-    const int64_t at = ((int64_t)b * a.q_tokens + i) * a.q_heads + kvh * a.group + r - i * a.group;
-    const AttnScale f = attn_scale<kNv>(a, kvh, mm, mx, ll);
-    TQ *dst = static_cast<TQ *>(a.out) + at * D;
-    for (int d = (int)threadIdx.x; d < D; d += kAttnThreads) {
-        float y = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w)
-            y += s_v[w][d];
-        dst[d] = to_out<TQ>(y * f.f * f.f2);
-    }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[at] = attn_lse(mm, ll);
+    } while (share.left > 0);
 }
 
 } // namespace fp4

@@ -15,6 +15,21 @@ __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b)
     return r;
 }
 
+// The pair a times one half of b (the high one if `high`).
+__device__ __forceinline__ uint32_t f16x2_mul_half(uint32_t a, uint32_t b, bool high)
+{
+    uint32_t r;
+    if (high)
+        asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 s;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 s, {h, h};\n\tmul.rn.f16x2 %0, %1, s;\n\t}"
+            : "=r"(r)
+            : "r"(a), "r"(b));
+    else
+        asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 s;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 s, {l, l};\n\tmul.rn.f16x2 %0, %1, s;\n\t}"
+            : "=r"(r)
+            : "r"(a), "r"(b));
+    return r;
+}
+
 // (lo, hi) -> f16x2, round to nearest even.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {

@@ -525,8 +525,10 @@ fp4_status fp4_kv_read(const fp4_kv_cache *cache, const int64_t *slots, int64_t 
  *        reads KV head h / (q_heads / heads)
  *   out  as q, contiguous and 16-byte aligned; lse fp32 [batch, q_tokens,
  *        q_heads] or NULL
- *   page_table  int32 [batch, table_width]; seq_lens int32 [batch]
- * head_dim 64, 128 or 256 (else FP4_ERR_SHAPE); softmax_scale finite.
+ *   page_table  int32 [batch, table_width], table_width * page_size at most
+ *        2^30 (else FP4_ERR_SHAPE); seq_lens int32 [batch]
+ * head_dim 64, 128 or 256, batch and heads * (rows of 16 below) at most
+ * 65535 (else FP4_ERR_SHAPE); softmax_scale finite.
  * A length below 0 or above table_width * page_size sets INDEX, as does a
  * page outside the cache that a visible position names; that sequence's
  * outputs are then unspecified, the others' are not.  A NaN or Inf in a
@@ -537,9 +539,11 @@ fp4_status fp4_kv_read(const fp4_kv_cache *cache, const int64_t *slots, int64_t 
  * is rounded off.
  * Written for few new tokens: the cache is read once for every 16 rows of
  * q_tokens * q_heads / heads (8 for head_dim 256 or fp32 q); a long prompt reads it back with fp4_kv_read for
- * a dense attention.  One kernel, and a second one where the tokens are
- * split over CTAs; the workspace (any contents) holds the splits' results,
- * and its size depends on head_dim alone. */
+ * a dense attention.  One kernel.  The workspace holds the results of
+ * sequences that several CTAs share and a counter for each (sequence, head);
+ * it must be zero-filled once before its first use, every call leaves its
+ * counters at zero, and any calls on caches of one head_dim may take turns on
+ * it. */
 size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache *cache, int64_t batch, int64_t q_tokens, int64_t q_heads,
                                         int64_t table_width);
 fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const void *q, fp4_dtype dtype, int64_t batch,
