@@ -202,6 +202,7 @@ fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t ro
     a.chunks = l.chunks;
     a.tiles = (int)((Kp / group + 3) / 4);
     a.out_bf16 = out_dtype == FP4_BF16;
+    a.accs = fp4::lin_accumulators(l.cols, out_dtype == FP4_F32);
     a.status = status;
     a.splits = pick_splits(bands * l.tiles, a.chunks, (int64_t)sms * (a.cols <= fp4::kLinSharedCols ? 2 : 1));
     a.share = a.chunks / a.splits;

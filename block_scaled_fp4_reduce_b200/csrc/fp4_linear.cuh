@@ -75,11 +75,19 @@ __host__ __device__ constexpr int lin_stage_bytes(int cols, bool fused)
 {
     return kLinCodes + kLinScales + (fused ? 0 : cols * kLinChunk * 2);
 }
-// Tensor memory: the accumulator, then three decoded chunks of 64 columns (two
-// beyond 64 columns, where the CTA has an SM's 512 columns for itself anyway).
+// Tensor memory: accumulators, then three decoded chunks of 64 columns.  The
+// tensor core cuts a sum off rather than rounding it, which over the 112 MMAs
+// of a share of 1792 elements costs 1.6e-6 of the result; with fp32 results
+// the MMAs of a chunk therefore take turns on up to four accumulators, as many
+// as fit (4e-7 with four).
 constexpr int kLinSharedCols = 64; // the largest tile with two CTAs on an SM
-__host__ __device__ constexpr int lin_tmem_cols(int cols) { return cols <= kLinSharedCols ? 256 : 512; }
 constexpr int kLinBuffers = 3;
+__host__ __device__ constexpr int lin_tmem_cols(int cols) { return cols <= kLinSharedCols ? 256 : 512; }
+__host__ __device__ constexpr int lin_accumulators(int cols, bool f32)
+{
+    const int fit = (lin_tmem_cols(cols) - 64 * kLinBuffers) / cols;
+    return !f32 || fit < 2 ? 1 : fit < 4 ? 2 : 4; // a power of two: MMA k of a chunk takes k modulo it
+}
 
 template <typename T> __device__ __forceinline__ float to_f32(T v)
 {
@@ -231,6 +239,7 @@ struct LinearArgs {
     int most_share;   // chunks that the fused layout's memory holds
     int own, own_inv;   // weight rows that a CTA owns, and 2^16 / own rounded up
     uint32_t own_magic; // 2^32 / own rounded up (own = 1 does not occur)
+    int accs;           // accumulators
     int out_bf16;
     int32_t *status;
 };
@@ -366,7 +375,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot, tmem_a = tmem + (uint32_t)a.cols;
+    const uint32_t tmem = tmem_slot, tmem_a = tmem + tmem_cols - 64 * kLinBuffers;
     cluster_arrive(); // this CTA runs, its barriers are there: the others may copy into its shared memory
 
     bool timed_out = false;
@@ -439,8 +448,8 @@ __global__ void __launch_bounds__(kLinThreads, 2)
                 const uint64_t x = x0 + (uint64_t)((uint32_t)(kFused ? i : s) * step);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    tc_mma_f16_ts(tmem, tmem_a + (uint32_t)(64 * b + 8 * k),
-                                  x + (uint64_t)((k >> 2) * half + (uint32_t)(k & 3) * 2), idesc, (i | k) != 0);
+                    tc_mma_f16_ts(tmem + (uint32_t)((k & (a.accs - 1)) * a.cols), tmem_a + (uint32_t)(64 * b + 8 * k),
+                                  x + (uint64_t)((k >> 2) * half + (uint32_t)(k & 3) * 2), idesc, i > 0 || k >= a.accs);
                 tc_commit(&empty[s]);
             }
             __syncwarp();
@@ -571,6 +580,13 @@ __global__ void __launch_bounds__(kLinThreads, 2)
                 continue; // columns without a row
             float v[8];
             tc_load_8(tmem + (uint32_t)c + ((uint32_t)(quarter * 32) << 16), v);
+            for (int q = 1; q < a.accs; ++q) {
+                float more[8];
+                tc_load_8(tmem + (uint32_t)(q * a.cols + c) + ((uint32_t)(quarter * 32) << 16), more);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] += more[j];
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float2 f = s_factor[c + j];
