@@ -330,6 +330,74 @@ def test_attention_repeats_bit_for_bit_and_its_workspace_serves_smaller_calls():
     check_attention(c, q, table, [4400, 100, 2000], 128 ** -0.5, 0)
 
 
+@pytest.mark.parametrize("B,longest,heads,group", [(40, 900, 2, 3), (150, 700, 1, 2), (300, 300, 1, 1)])
+def test_attention_of_many_sequences(B, longest, heads, group):
+    """Batches beyond a warp's and beyond a CTA's scan of the lengths; sequences share pages."""
+    g = gen(B)
+    c = make_cache(g, 30, heads, 64, 32, NV)
+    width = -(-longest // 32)
+    table = torch.randint(0, 30, (B, width), generator=g, dtype=torch.int32).cuda()
+    lens = torch.randint(0, longest + 1, (B,), generator=g).tolist()
+    lens[3], lens[B - 1] = 0, longest
+    check_attention(c, randn(g, B, 1, heads * group, 64), table, lens, 0.003, 0)
+
+
+def test_attention_of_more_units_than_the_gpu_holds_at_once():
+    g = gen(41)
+    B, heads = 1600, 4
+    c = make_cache(g, 9, heads, 64, 16, NV)
+    table = torch.randint(0, 9, (B, 20), generator=g, dtype=torch.int32).cuda()
+    lens = torch.randint(0, 24, (B,), generator=g).tolist()
+    lens[1111] = 320
+    check_attention(c, randn(g, B, 1, heads, 64), table, lens, 0.003, 0)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+@pytest.mark.parametrize("n,new,group,window", [(12900, 1, 1, 0), (60001, 1, 2, 0), (9000, 3, 7, 0), (70000, 1, 1, 40000)])
+def test_attention_of_one_sequence_in_many_pieces(n, new, group, window, fmt):
+    """One sequence and head over the whole GPU: dozens to hundreds of pieces to join."""
+    g = gen(n)
+    c = make_cache(g, 50, 1, 64, 64, fmt)
+    table = torch.randint(0, 50, (1, -(-n // 64)), generator=g, dtype=torch.int32).cuda()
+    check_attention(c, randn(g, 1, new, group, 64), table, [n], 0.003, window)
+
+
+def test_attention_calls_of_different_shapes_take_turns_on_one_workspace():
+    g = gen(43)
+    c = make_cache(g, 60, 2, 128, 64, NV)
+    big, small = tables(g, 4, 50, 60), tables(g, 1, 50, 60)
+    qb, qs = randn(g, 4, 2, 16, 128), randn(g, 1, 1, 4, 128)
+    lb = torch.tensor([3200, 64, 1999, 0], dtype=torch.int32).cuda()
+    ls = torch.tensor([3111], dtype=torch.int32).cuda()
+    want_b, want_s = fp4.kv_attention(qb, c, big, lb), fp4.kv_attention(qs, c, small, ls)
+    want_f = fp4.kv_attention(qs.float(), c, small, ls)
+    ws = fp4.kv_attention_workspace(qb, c, big)
+    for _ in range(4):
+        for args, want in (((qs, c, small, ls), want_s), ((qb, c, big, lb), want_b), ((qs.float(), c, small, ls), want_f)):
+            got = fp4.kv_attention(*args, workspace=ws)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_attention_captured_once_follows_growing_lengths():
+    g = gen(44)
+    c = make_cache(g, 70, 2, 64, 16, NV)
+    table = tables(g, 2, 60, 70)
+    q = randn(g, 2, 1, 6, 64)
+    lens = torch.tensor([5, 0], dtype=torch.int32).cuda()
+    ws = fp4.kv_attention_workspace(q, c, table)
+    fp4.kv_attention(q, c, table, lens, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = fp4.kv_attention(q, c, table, lens, workspace=ws)
+    for n in ([5, 0], [300, 17], [960, 959], [1, 513]):
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_attention(c, q, table, n, 0.125, 0, got=(out, lse))
+    del graph
+
+
 # ------------------------------------------------------------------- linear --
 
 def make_weight(g, n, k, fmt, dtype=BF):
@@ -375,6 +443,37 @@ def test_linear_of_a_padded_weight_and_strided_rows(fmt, k, dtype):
     x[:, k:] = float("nan")  # beside the rows
     check_linear(x[:, :k], w, dec, dtype)
     check_linear(x[::2, :k], w, dec, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+@pytest.mark.parametrize("rows,n,k", [(200, 70, 160), (401, 129, 96), (3, 40, 20000), (2, 20000, 160), (1, 4000, 14464), (90, 1300, 4096), (40, 300, 2080)])
+def test_linear_beyond_one_tile(rows, n, k, fmt, dtype):
+    """Several tiles of rows, long and short K, more bands than SMs, K shares of unequal length."""
+    g = gen(rows + n + k)
+    w, dec = make_weight(g, n, k, fmt)
+    check_linear(randn(g, rows, k, dtype=dtype), w, dec, F32)
+
+
+def test_calls_on_a_given_stream():
+    g = gen(27)
+    w, dec = make_weight(g, 300, 512, NV)
+    x = randn(g, 3, 512)
+    c = make_cache(g, 4, 2, 64, 16, NV)
+    table = tables(g, 1, 4, 4)
+    q = randn(g, 1, 1, 2, 64)
+    lens = torch.tensor([60], dtype=torch.int32).cuda()
+    want = fp4.linear(x, w), fp4.kv_attention(q, c, table, lens)[0]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for given in (s, s.cuda_stream):
+        y, o = torch.empty_like(want[0]), torch.empty_like(want[1])
+        ws = fp4.linear_workspace(3, w), fp4.kv_attention_workspace(q, c, table)
+        torch.cuda.synchronize()
+        fp4.linear(x, w, out=y, workspace=ws[0], stream=given)
+        fp4.kv_attention(q, c, table, lens, out=o, workspace=ws[1], stream=given)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(o, want[1])
 
 
 def test_linear_rows_of_every_size_and_empty_ones():
@@ -448,6 +547,34 @@ def test_linear_writes_its_output_alone():
     buf = torch.full((3 * 77 + 64,), 5.0, dtype=BF, device="cuda")
     fp4.linear(randn(g, 3, 96), w, out=buf[32:32 + 231].view(3, 77))
     assert (buf[:32] == 5).all() and (buf[32 + 231:] == 5).all()
+
+
+def test_the_helpers_refuse_what_does_not_fit():
+    g = gen(28)
+    w, _ = make_weight(g, 70, 64, NV)
+    x = randn(g, 3, 64)
+    for bad in (lambda: fp4.linear(x[:, :32], w), lambda: fp4.linear(x.half(), w), lambda: fp4.linear(x.t().contiguous().t(), w),
+                lambda: fp4.linear(x, w, out=torch.empty(3, 71, dtype=BF, device="cuda")), lambda: fp4.linear(x.cpu(), w),
+                lambda: fp4.linear(x, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")[8:])):
+        with pytest.raises((ValueError, TypeError, fp4.FP4Error)):
+            bad()
+    c = make_cache(g, 4, 2, 64, 16, NV)
+    k, slots = randn(g, 3, 2, 64), torch.tensor([1, 2, 3]).cuda()
+    table, lens, q = tables(g, 1, 4, 4), torch.tensor([60], dtype=torch.int32).cuda(), randn(g, 1, 1, 4, 64)
+    for bad in (lambda: fp4.kv_write(c, k, k.float(), slots), lambda: fp4.kv_write(c, k[:, :1], k[:, :1], slots),
+                lambda: fp4.kv_write(c, k, k, slots.int()), lambda: fp4.kv_write(c, k, k, slots.cpu()),
+                lambda: fp4.kv_write(c, k.transpose(1, 2).contiguous().transpose(1, 2), k, slots), lambda: fp4.kv_write(c, k, k, slots, rule=5),
+                lambda: fp4.kv_read(c, slots, out_dtype=torch.float16), lambda: fp4.kv_attention(q[..., :32], c, table, lens),
+                lambda: fp4.kv_attention(q, c, table.long(), lens), lambda: fp4.kv_attention(q, c, table, lens.repeat(2)),
+                lambda: fp4.kv_attention(q[:, :, :3], c, table, lens), lambda: fp4.kv_attention(q, c, table, lens, window=-1),
+                lambda: fp4.kv_attention(q, c, table, lens, scale=float("nan")), lambda: fp4.kv_attention(q.half(), c, table, lens),
+                lambda: fp4.kv_attention(q, c, table, lens, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda")),
+                lambda: fp4.KVCache(NV, c.k_packed, c.k_scales, c.v_packed, c.v_scales), lambda: fp4.KVCache(MX, c.k_packed, c.k_scales, c.v_packed, c.v_scales),
+                lambda: fp4.LinearWeight(NV, w.packed, w.scales_mma[:-1], w.global_scale, 70, 64)):
+        with pytest.raises((ValueError, TypeError, fp4.FP4Error)):
+            bad()
+    c.check()
+    w.check()
 
 
 # ------------------------------------------------------------- all together --
