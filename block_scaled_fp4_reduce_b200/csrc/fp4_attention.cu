@@ -120,7 +120,7 @@ fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const void *q, fp4_dtype 
                             void *out, float *lse, void *workspace, size_t workspace_bytes, int32_t *status,
                             cudaStream_t stream)
 {
-    if (!valid_dtype(dtype) || !status || window < 0 || !std::isfinite(softmax_scale))
+    if (!valid_dtype(dtype) || !status || window < 0 || !std::isfinite(softmax_scale * 1.5f)) // log2(e) joins the scale
         return FP4_ERR_INVALID_ARG;
     fp4_status st = check_attention(cache, batch, q_tokens, q_heads, table_width);
     if (st != FP4_OK || batch == 0 || q_tokens == 0)
@@ -162,6 +162,7 @@ fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const void *q, fp4_dtype 
     a.stats = reinterpret_cast<float4 *>(static_cast<char *>(workspace) + p.stats);
     a.status = status;
     a.group = (int)(q_heads / cache->heads);
+    a.group_magic = ~(uint64_t)0 / (uint64_t)a.group + 1;
     a.rows = p.rows;
     a.row_tiles = p.row_tiles;
     a.arrived = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + p.arrived);

@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
             const int tiles = min(c0 + n, a.tiles) - c0;
 #pragma unroll 8
             for (int i = 0; i < tiles; ++i)
-                m4 = __vmaxu4(m4, __ldg(reinterpret_cast<const uint32_t *>(p + (int64_t)i * 512)));
+                m4 = __vmaxu4(m4, __ldcg(reinterpret_cast<const uint32_t *>(p + (int64_t)i * 512)));
             top = max(max(m4 & 0xFFu, (m4 >> 8) & 0xFFu), max((m4 >> 16) & 0xFFu, m4 >> 24));
         }
         // positions of this chunk in the ring and among the buffers, and of the

@@ -528,7 +528,8 @@ fp4_status fp4_kv_read(const fp4_kv_cache *cache, const int64_t *slots, int64_t 
  *   page_table  int32 [batch, table_width], table_width * page_size at most
  *        2^30 (else FP4_ERR_SHAPE); seq_lens int32 [batch]
  * head_dim 64, 128 or 256, batch and heads * (rows of 16 below) at most
- * 65535 (else FP4_ERR_SHAPE); softmax_scale finite.
+ * 65535 (else FP4_ERR_SHAPE); softmax_scale finite
+ * (and 1.5 times it).
  * A length below 0 or above table_width * page_size sets INDEX, as does a
  * page outside the cache that a visible position names; that sequence's
  * outputs are then unspecified, the others' are not.  A NaN or Inf in a
@@ -563,6 +564,8 @@ fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const void *q, fp4_dtype 
  * The activations enter the tensor cores as fp16 after a power of two per
  * row (fp32 x as two terms, 22 bits): bf16 x is exact but for what lies
  * below 2^-38 of its row's largest value.  Products are summed in fp32.
+ * MXFP4: within a row of the weight, what a block holds below 2^-24 of the
+ * row's largest block scale is rounded off.
  * A NaN or Inf in x sets NONFINITE (its row of y is then unspecified, the
  * others are not).  N and rows
  * below 2^23, K below 2^31 - 1024 (else FP4_ERR_SHAPE).  rows or N = 0: nothing is done;
