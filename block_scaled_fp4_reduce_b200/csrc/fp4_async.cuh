@@ -57,6 +57,29 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32
     return false;
 }
 
+// The same for two barriers, asked one behind the other: where both phases are
+// complete already, which a loop that runs behind its producers finds, the two
+// answers take the time of one.
+__device__ __forceinline__ bool mbar_wait_both(uint64_t *bar_a, uint32_t parity_a, uint64_t *bar_b, uint32_t parity_b)
+{
+    for (uint32_t t = 0; t < kWaitTries; ++t) {
+        uint32_t done;
+        asm volatile("{\n\t"
+                     ".reg .pred p, q;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+                     "and.pred p, p, q;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t"
+                     "}"
+                     : "=r"(done)
+                     : "r"(smem_addr(bar_a)), "r"(parity_a), "r"(smem_addr(bar_b)), "r"(parity_b)
+                     : "memory");
+        if (done)
+            return true;
+    }
+    return false;
+}
+
 // Makes the barriers' initialisation visible to the copy engine.
 __device__ __forceinline__ void mbar_init_fence()
 {

@@ -431,40 +431,36 @@ __global__ void __launch_bounds__(kLinThreads, 2)
         const uint32_t half = (uint32_t)a.cols * kLinChunk / 16, step = kFused ? 2 * half : (uint32_t)stage_bytes / 16;
         if (kFused && !__all_sync(0xFFFFFFFFu, mbar_wait(&laid, 0)))
             timed_out = true;
-        uint32_t phase = 0, ready_phase = 0;
-        for (int i = 0, s = 0, b = 0; i < n && !timed_out; ++i) {
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[s], phase))) {
-                timed_out = true;
-                break;
-            }
-            if (lane == 0)
-                consumed = i + 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ready[b], ready_phase))) {
-                timed_out = true;
-                break;
-            }
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t x = x0 + (uint64_t)((uint32_t)(kFused ? i : s) * step);
+        // One thread runs the loop: votes and re-elections between its steps cost
+        // more than the steps.
+        if (elect_one()) {
+            int i = 0;
+            for (uint32_t s = 0, b = 0, phase = 0, ready_phase = 0; i < n && !timed_out; ++i) {
+                if (!mbar_wait_both(&ready[b], ready_phase, &full[s], phase)) {
+                    timed_out = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t x = x0 + (uint64_t)((kFused ? (uint32_t)i : s) * step);
+                const uint32_t w = tmem_a + 64 * b;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    tc_mma_f16_ts(tmem + (uint32_t)((k & (a.accs - 1)) * a.cols), tmem_a + (uint32_t)(64 * b + 8 * k),
+                    tc_mma_f16_ts(tmem + (uint32_t)((k & (a.accs - 1)) * a.cols), w + (uint32_t)(8 * k),
                                   x + (uint64_t)((k >> 2) * half + (uint32_t)(k & 3) * 2), idesc, i > 0 || k >= a.accs);
                 tc_commit(&empty[s]);
+                if (++s == (uint32_t)stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+                if (++b == kLinBuffers) {
+                    b = 0;
+                    ready_phase ^= 1u;
+                }
             }
-            __syncwarp();
-            if (++s == stages) {
-                s = 0;
-                phase ^= 1u;
-            }
-            if (++b == kLinBuffers) {
-                b = 0;
-                ready_phase ^= 1u;
-            }
-        }
-        if (elect_one())
+            consumed = i;
             tc_commit(&done);
-        __syncwarp();
+        }
+        timed_out = __any_sync(0xFFFFFFFFu, timed_out);
     } else {
         const int group = warp >> 2, quarter = warp & 3; // rows 32 quarter .. + 31: the tensor-memory lanes this warp reaches
         const int row = quarter * 32 + lane, word = lane * 16 + quarter * 4; // its scale word in a tile
@@ -484,10 +480,9 @@ __global__ void __launch_bounds__(kLinThreads, 2)
         int s = group, b = group, old = group;
         uint32_t phase = 0, old_phase = 0;
         for (int i = group; i < n; i += 2) {
-            bool ok = mbar_wait(&full[s], phase);
-            if (i >= kLinBuffers) { // the MMA has read what the buffer held, chunk i - 3
-                ok = ok && mbar_wait(&empty[old], old_phase);
-            }
+            // (from chunk 3 on: and the MMA has read what the buffer held, chunk i - 3)
+            const bool ok = i >= kLinBuffers ? mbar_wait_both(&full[s], phase, &empty[old], old_phase)
+                                             : mbar_wait(&full[s], phase);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 timed_out = true;
                 break;
