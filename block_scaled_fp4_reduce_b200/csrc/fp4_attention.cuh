@@ -79,7 +79,9 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnStep = 32;       // tokens of a warp's step
 constexpr int kAttnRound = kAttnWarps * kAttnStep; // of a step of all warps
-constexpr int kAttnMinShare = 2;    // rounds: a CTA's start and end cost about as much as two
+constexpr int kAttnMinShare = 2;    // rounds of a CTA's share, at least
+constexpr int kAttnStart = 2;       // what a unit's start and end count as, in rounds
+constexpr int kAttnWhole = 8;       // rounds up to which a unit is left to one CTA
 // Weights enter the tensor cores times 2^kAttnBias, and pass the reference
 // by at most 2^kAttnSlack: 2^15 is the largest power of two in fp16.
 constexpr float kAttnBias = 11.0f, kAttnSlack = 4.0f;
@@ -227,20 +229,23 @@ template <typename TQ> __device__ __forceinline__ void attn_write(TQ *dst, float
 
 // ---------------------------------------------------------------------------
 // How the tokens are shared out.  A unit is one sequence, row tile and KV head;
-// its work is its rounds.  With the units in that order (heads innermost) and
-// all rounds numbered through, CTA i takes rounds [i s, (i + 1) s), s = the
-// total over the CTAs that fit on the GPU: every CTA has the same work whatever
-// the lengths are, in one wave.  The lengths are on the device, so every CTA
-// forms the numbering for itself, a scan over the sequences.  A CTA whose
-// rounds cross units takes them one after the other; a unit that crosses CTAs
-// leaves pieces, which the CTA that finishes the last of them joins.
+// its work is its rounds, and kAttnStart more for its start and end.  With the
+// units in that order (heads innermost) and all of this numbered through, CTA i
+// takes the numbers [i s, (i + 1) s), s = the total over the CTAs that fit on
+// the GPU: every CTA has the same work whatever the lengths are, in one wave
+// (short sequences beside long ones: 256 sequences of 0 to 2000 tokens, 8 heads x
+// 128, 4 query heads each, take 131 us where starts count for nothing, 84 so; 3
+// and 4 rounds for a start are no better than 2).  The lengths are on the device, so
+// every CTA forms the numbering for itself, a scan over the sequences.  A CTA
+// whose numbers cross units takes them one after the other; a unit that crosses
+// CTAs leaves pieces, which the CTA that finishes the last of them joins.
 // ---------------------------------------------------------------------------
 template <int R> __device__ __forceinline__ uint32_t attn_sequence_rounds(const AttnArgs &a, int len)
 {
     uint32_t sum = 0;
     for (int rt = 0; rt < a.row_tiles; ++rt) {
         const int row0 = rt * R, rows = min(R, a.rows - row0);
-        sum += (uint32_t)attn_rounds(attn_span(a, len, attn_token(a, row0), attn_token(a, row0 + rows - 1)));
+        sum += (uint32_t)attn_rounds(attn_span(a, len, attn_token(a, row0), attn_token(a, row0 + rows - 1))) + kAttnStart;
     }
     return sum * (uint32_t)a.c.heads;
 }
@@ -270,13 +275,13 @@ __device__ __forceinline__ uint32_t attn_scan(uint32_t v, uint32_t *s_warp, uint
     return v;
 }
 
-// This CTA's share: the sequence its first round lies in, that round's number
-// within the sequence, the rounds from there on, and the CTAs' common share;
-// false if there are none.  (The host sees to it that all rounds number below
+// This CTA's share: the sequence its first number lies in, that number within
+// the sequence, how many there are from there on, and the CTAs' common share;
+// false if there are none.  (The host sees to it that the numbers stay below
 // 2^31.)
 struct AttnShare {
     int b, len; // len: of sequence b
-    uint32_t at, left, each, done; // done: rounds this CTA has behind it
+    uint32_t at, left, each, done; // done: numbers this CTA has behind it
 };
 
 template <int R> __device__ __forceinline__ bool attn_share(const AttnArgs &a, AttnShare &out)
@@ -519,18 +524,24 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
             len = 0; // read below, after the query rows are asked for
         }
         int from = 0, to = 0, all_rounds = 0; // rounds of the unit
+        int number = 0, numbers = 0;          // where the share meets the unit's numbers, and how many it takes
         if (a.split) {
-            uint32_t at = share.at;
+            uint32_t at = share.at, unit;
             for (;; ++rt) {
                 const AttnSpan s = attn_span(a, len, attn_token(a, rt * R), attn_token(a, min(rt * R + R, a.rows) - 1));
                 all_rounds = attn_rounds(s);
-                if (at < (uint32_t)all_rounds * a.c.heads)
+                unit = (uint32_t)(all_rounds + kAttnStart);
+                if (at < unit * a.c.heads)
                     break;
-                at -= (uint32_t)all_rounds * a.c.heads;
+                at -= unit * a.c.heads;
             }
-            kvh = (int)(at / (uint32_t)all_rounds);
-            from = (int)at - kvh * all_rounds;
-            to = (int)min((uint32_t)all_rounds, from + share.left);
+            kvh = (int)(at / unit);
+            number = (int)(at - kvh * unit);
+            numbers = (int)min(unit - number, share.left);
+            from = max(number - kAttnStart, 0);
+            to = number + numbers - kAttnStart;
+            if (to <= 0) // the share ends before the unit's first round
+                return;
         }
         const int row0 = rt * R, rows = min(R, a.rows - row0);
         const int i0 = attn_token(a, row0); // new token of the first row
@@ -1153,8 +1164,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
         }
         if (a.split) {
             if (!whole) {
-                // the unit's first round's number among all, and the CTAs that have pieces of it
-                const uint32_t u0 = share.each * blockIdx.x + share.done - (uint32_t)from;
+                // the unit's first round among all numbers, and the CTAs that have pieces of it
+                const uint32_t u0 = share.each * blockIdx.x + share.done - (uint32_t)number + kAttnStart;
                 const uint32_t first = u0 / share.each, last_cta = (u0 + (uint32_t)all_rounds - 1) / share.each;
                 __shared__ bool s_last;
                 __syncthreads();
@@ -1171,9 +1182,9 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
                     attn_merge<TQ, kNv, D, R>(a.partial, a.stats, static_cast<TQ *>(a.out), a.lse, smem, s_row, gv, rows,
                                               (int)first, (int)(last_cta - first) + 1);
             }
-            share.left -= to - from;
-            share.at += to - from;
-            share.done += to - from;
+            share.left -= numbers;
+            share.at += numbers;
+            share.done += numbers;
             if (kvh == a.c.heads - 1 && rt == a.row_tiles - 1 && to == all_rounds) {
                 share.at = 0;
                 if (++share.b < a.batch)

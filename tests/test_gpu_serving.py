@@ -352,6 +352,35 @@ def test_attention_of_more_units_than_the_gpu_holds_at_once():
     check_attention(c, randn(g, B, 1, heads, 64), table, lens, 0.003, 0)
 
 
+WIDE = [  # lens, new, heads, group, dim, window: tables for 1500 tokens, whatever is there of them
+    ([0, 1, 15, 16, 17, 0, 127, 128, 129, 300, 1500], 1, 2, 3, 64, 0),
+    ([1], 1, 1, 1, 128, 0),
+    ([130], 1, 8, 4, 128, 0),
+    ([257, 1499, 3], 4, 3, 5, 128, 0),
+    ([0, 0, 0], 2, 2, 2, 64, 0),
+    ([1500, 700, 20], 1, 2, 8, 256, 0),
+    ([1500, 700, 20], 2, 1, 9, 128, 1100),
+    ([0] * 60 + [1500] + [2] * 40, 1, 4, 2, 64, 0),
+    ([129] * 90, 1, 2, 1, 128, 0),
+    ([1 + 11 * i for i in range(130)], 1, 3, 1, 64, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+@pytest.mark.parametrize("lens,new,heads,group,dim,window", WIDE)
+def test_attention_of_short_sequences_under_a_wide_table(lens, new, heads, group, dim, window, fmt, dtype):
+    """The tokens are shared out over all CTAs: shares that end inside a unit's start, cross many units, or are a part of one."""
+    g = gen(len(lens) + dim + new)
+    c = make_cache(g, 40, heads, dim, 48, fmt)
+    table = torch.randint(0, 40, (len(lens), 32), generator=g, dtype=torch.int32).cuda()
+    for b, n in enumerate(lens):
+        table[b, -(-n // 48):] = -1
+    check_attention(c, randn(g, len(lens), new, heads * group, dim, dtype=dtype), table, lens, 1 / np.sqrt(dim) / 40, window)
+    torch.cuda.synchronize()
+    c.check()
+
+
 @pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
 @pytest.mark.parametrize("n,new,group,window", [(12900, 1, 1, 0), (60001, 1, 2, 0), (9000, 3, 7, 0), (70000, 1, 1, 40000)])
 def test_attention_of_one_sequence_in_many_pieces(n, new, group, window, fmt):
