@@ -66,9 +66,12 @@ __host__ __device__ constexpr int lin_landing_bytes(int cols) { return cols <= k
 
 // Where a CTA's share of the activations is small, the decoders lay it out
 // themselves, in shared memory, while the first codes are on their way: no
-// packing grid and no workspace.  The most columns, chunks of K, and rows x
-// chunks (beyond that the layout takes longer than the packing grid).
-constexpr int kLinFusedCols = 16, kLinFusedShare = 16, kLinFusedWork = 32;
+// packing grid and no workspace.  The most rows, and rows x chunks of K.  Laid
+// out by the decoders | packed, us, cold L2, bf16: 1 x 8192 x 4096 (8 chunks a
+// CTA) 14.5 | 16.3, 1 x 14336 x 4096 (16) 18.4 | 18.4, 2 x 8192 x 4096 16.3 |
+// 16.4, 2 x 14336 x 4096 20.4 | 19.5, 4 x 4096 x 4096 (4) 16.4 | 14.3, 8 x 4096
+// x 4096 20.4 | 15.3.
+constexpr int kLinFusedRows = 2, kLinFusedShare = 16;
 
 // Codes and scales of a chunk, with its activations where those come packed.
 __host__ __device__ constexpr int lin_stage_bytes(int cols, bool fused)
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kLinThreads, 2)
     __shared__ __align__(8) uint64_t full[kLinMaxStages], empty[kLinMaxStages], ready[kLinBuffers], done, laid, landed;
     __shared__ uint32_t tmem_slot;
     __shared__ float2 s_factor[kLinMaxCols]; // the column's power of two, in two factors
-    __shared__ uint32_t s_top[kLinFusedCols];
+    __shared__ uint32_t s_top[kLinFusedRows];
     __shared__ float s_g;
     __shared__ int consumed; // chunks whose copies the MMA warp has seen land
     uint8_t *const smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
