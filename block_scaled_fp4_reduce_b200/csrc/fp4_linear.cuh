@@ -31,6 +31,15 @@
 // of their row in the CTA's share of K (found by a scan of the scale bytes
 // before the first chunk), 2^(e - E), which is exact down to 2^-23; the row's
 // 2^E multiplies the sum.
+//
+// What bounds it (cold L2): a weight of 57344 x 14336, 462 MB, takes 109 us with
+// one activation row, 157 with 64 (copies alone 82).  The ring keeps HBM busy
+// while a CTA is in its loop; the starts and ends of its units, about as long as
+// six chunks each, and the last round of the grid are the rest.  With 64 rows the
+// activations that every band of 128 weight rows reads again from L2 are 1.8
+// times the weight's bytes.  A weight of 14336 x 4096 takes 16.6 us with 16 rows,
+// 5 of them its bytes: launch, packing and the first copies 3 us, the sums'
+// way through the cluster 3.
 #pragma once
 
 #include <cstdint>

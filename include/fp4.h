@@ -528,8 +528,7 @@ fp4_status fp4_kv_read(const fp4_kv_cache *cache, const int64_t *slots, int64_t 
  *   page_table  int32 [batch, table_width], table_width * page_size at most
  *        2^30 (else FP4_ERR_SHAPE); seq_lens int32 [batch]
  * head_dim 64, 128 or 256, batch and heads * (rows of 16 below) at most
- * 65535 (else FP4_ERR_SHAPE); softmax_scale finite
- * (and 1.5 times it).
+ * 65535 (else FP4_ERR_SHAPE); softmax_scale finite (and 1.5 times it).
  * A length below 0 or above table_width * page_size sets INDEX, as does a
  * page outside the cache that a visible position names; that sequence's
  * outputs are then unspecified, the others' are not.  A NaN or Inf in a
@@ -539,8 +538,9 @@ fp4_status fp4_kv_read(const fp4_kv_cache *cache, const int64_t *slots, int64_t 
  * and head, what a block holds below 2^-24 of the head's largest block scale
  * is rounded off.
  * Written for few new tokens: the cache is read once for every 16 rows of
- * q_tokens * q_heads / heads (8 for head_dim 256 or fp32 q); a long prompt reads it back with fp4_kv_read for
- * a dense attention.  One kernel.  The workspace holds the results of
+ * q_tokens * q_heads / heads (8 for head_dim 256 or fp32 q); a long prompt
+ * reads it back with fp4_kv_read for a dense attention.  One kernel.  The
+ * workspace holds the results of
  * sequences that several CTAs share and a counter for each (sequence, head);
  * it must be zero-filled once before its first use, every call leaves its
  * counters at zero, and any calls on caches of one head_dim may take turns on
@@ -567,10 +567,10 @@ fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const void *q, fp4_dtype 
  * MXFP4: within a row of the weight, what a block holds below 2^-24 of the
  * row's largest block scale is rounded off.
  * A NaN or Inf in x sets NONFINITE (its row of y is then unspecified, the
- * others are not).  N and rows
- * below 2^23, K below 2^31 - 1024 (else FP4_ERR_SHAPE).  rows or N = 0: nothing is done;
- * K = 0: y = 0.  Reads the weight once for every 160 rows (80 for fp32 x).  One kernel, or
- * two where the activations are laid out first, in the workspace (any contents). */
+ * others are not).  N and rows below 2^23, K below 2^31 - 1024 (else
+ * FP4_ERR_SHAPE).  rows or N = 0: nothing is done; K = 0: y = 0.  Reads the
+ * weight once for every 160 rows (80 for fp32 x).  One kernel, or two where
+ * the activations are laid out first, in the workspace (any contents). */
 size_t fp4_linear_workspace_bytes(int64_t rows, int64_t K);
 fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t rows, int64_t K, int64_t x_stride,
                       const uint8_t *packed, const uint8_t *scales_mma, const float *global_scale, int64_t N, void *y,

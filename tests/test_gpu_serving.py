@@ -505,6 +505,31 @@ def test_calls_on_a_given_stream():
         assert torch.equal(y, want[0]) and torch.equal(o, want[1])
 
 
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_calls_on_a_given_stream_allocate_for_it(handle):
+    """Without workspaces or outputs, the current stream held up: what the calls allocate belongs to the given stream."""
+    g = gen(76)
+    c = make_cache(g, 80, 2, 64, 32, NV)
+    w = fp4.linear_weight(fp4.nvfp4_quantize(randn(g, 300, 2048, scale=0.02)))
+    table, lens = tables(g, 2, 64, 80), torch.tensor([2000, 1200], dtype=torch.int32).cuda()
+    q, x, slots = randn(g, 2, 1, 8, 64), randn(g, 20, 2048), torch.arange(64).cuda()
+    want = [fp4.linear(x, w), *fp4.kv_attention(q, c, table, lens), *fp4.kv_read(c, slots)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    given = side.cuda_stream if handle else side
+    torch.cuda._sleep(20_000_000)
+    junk = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        got = [fp4.linear(x, w, stream=given), *fp4.kv_attention(q, c, table, lens, stream=given), *fp4.kv_read(c, slots, stream=given)]
+        del junk[:1]
+        side.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    torch.cuda.synchronize()
+    c.check()
+    w.check()
+
+
 def test_linear_rows_of_every_size_and_empty_ones():
     g = gen(21)
     for fmt in (NV, MX):
