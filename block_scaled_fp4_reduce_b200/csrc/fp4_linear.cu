@@ -131,7 +131,7 @@ extern "C" {
 
 size_t fp4_linear_workspace_bytes(int64_t rows, int64_t K)
 {
-    if (rows < 0 || K < 0 || rows > INT_MAX || K > INT_MAX - 1024)
+    if (rows < 0 || K < 0 || rows >= (1 << 23) || K > INT_MAX - 1024)
         return 0;
     const size_t one = layout(rows, K, 1).bytes, two = layout(rows, K, 2).bytes; // either type of x
     return one > two ? one : two;
@@ -147,8 +147,11 @@ fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t ro
         return FP4_ERR_INVALID_ARG;
     const int64_t group = fmt == FP4_NVFP4 ? 16 : 32;
     const int64_t in = dtype == FP4_BF16 ? 2 : 4, on = out_dtype == FP4_BF16 ? 2 : 4;
-    if (rows >= (1 << 23) || K > INT_MAX - 1024 || N >= (1 << 23))
+    const int parts = dtype == FP4_F32 ? 2 : 1;
+    if (rows >= (1 << 23) || K > INT_MAX - 1024 || N > (int64_t)65535 * fp4::kLinRows || // the grid's z, and its y
+        rows * parts > (int64_t)65535 * fp4::kLinMaxCols)
         return FP4_ERR_SHAPE;
+    const int64_t bands = (N + fp4::kLinRows - 1) / fp4::kLinRows;
     const int64_t Kp = (K + group - 1) / group * group;
     if (Kp % 32)
         return FP4_ERR_SHAPE;
@@ -180,11 +183,7 @@ fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t ro
     const int sms = sm_count(dev);
     if (sms <= 0)
         return FP4_ERR_CUDA;
-    const int parts = dtype == FP4_F32 ? 2 : 1;
     const Layout l = layout(rows, K, parts);
-    const int64_t bands = (N + fp4::kLinRows - 1) / fp4::kLinRows;
-    if (bands > 65535 || l.tiles > 65535)
-        return FP4_ERR_SHAPE;
     CUtensorMap map_w, map_x;
     std::memset(&map_w, 0, sizeof(map_w));
     std::memset(&map_x, 0, sizeof(map_x));

@@ -567,8 +567,8 @@ fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const void *q, fp4_dtype 
  * MXFP4: within a row of the weight, what a block holds below 2^-24 of the
  * row's largest block scale is rounded off.
  * A NaN or Inf in x sets NONFINITE (its row of y is then unspecified, the
- * others are not).  N and rows below 2^23, K below 2^31 - 1024 (else
- * FP4_ERR_SHAPE).  rows or N = 0: nothing is done; K = 0: y = 0.  Reads the
+ * others are not).  N at most 65535 * 128, rows below 2^23 (at most 65535 *
+ * 80 for fp32 x), K below 2^31 - 1024 (else FP4_ERR_SHAPE).  rows or N = 0: nothing is done; K = 0: y = 0.  Reads the
  * weight once for every 160 rows (80 for fp32 x).  One kernel, or two where
  * the activations are laid out first, in the workspace (any contents). */
 size_t fp4_linear_workspace_bytes(int64_t rows, int64_t K);

@@ -427,6 +427,27 @@ def test_attention_captured_once_follows_growing_lengths():
     del graph
 
 
+def test_attention_captured_once_follows_growing_lengths_under_a_wide_table():
+    """The tokens are shared out anew by every replay."""
+    g = gen(46)
+    c = make_cache(g, 70, 2, 64, 64, NV)
+    table = torch.randint(0, 70, (3, 80), generator=g, dtype=torch.int32).cuda()
+    q = randn(g, 3, 2, 6, 64)
+    lens = torch.tensor([5, 0, 1], dtype=torch.int32).cuda()
+    ws = fp4.kv_attention_workspace(q, c, table)
+    fp4.kv_attention(q, c, table, lens, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = fp4.kv_attention(q, c, table, lens, workspace=ws)
+    for n in ([5, 0, 1], [300, 17, 5120], [5120, 5119, 2], [0, 0, 0], [1, 1300, 129]):
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_attention(c, q, table, n, 0.125, 0, got=(out, lse))  # 64 ** -0.5, the default
+    del graph
+
+
 # ------------------------------------------------------------------- linear --
 
 def make_weight(g, n, k, fmt, dtype=BF):

@@ -112,6 +112,16 @@ def test_sizes_below_zero_and_overflow_give_no_workspace(L):
     assert L.fp4_linear_workspace_bytes(1 << 40, 32) == 0
 
 
+@pytest.mark.parametrize("rows,n,dt,want", [
+    (1, 65535 * 128, fp4.BF16, None), (1, 65535 * 128 + 1, fp4.BF16, fp4.ERR_SHAPE), (1, (1 << 63) - 1, fp4.BF16, fp4.ERR_SHAPE),
+    ((1 << 23) - 1, 8, fp4.BF16, None), (1 << 23, 8, fp4.BF16, fp4.ERR_SHAPE), (65535 * 80, 8, fp4.F32, None),
+    (65535 * 80 + 1, 8, fp4.F32, fp4.ERR_SHAPE)])
+def test_linear_s_largest_shapes(L, rows, n, dt, want):
+    """Up to the grid's limits a call gets as far as its workspace (refused here: none is given)."""
+    got = L.fp4_linear(fp4.NVFP4, P, dt, rows, 32, 32, P, P, P, n, P, fp4.BF16, None, 0, P, None)
+    assert got == (fp4.ERR_WORKSPACE if want is None else want)
+
+
 def test_status_string_of_a_bad_index(L):
     assert L.fp4_status_string(fp4.ERR_INDEX) == b"slot, page or length out of range"
 
