@@ -712,9 +712,9 @@ def kv_read(cache: KVCache, slots: torch.Tensor, out_dtype=torch.bfloat16, k=Non
             return kv_read(cache, slots, out_dtype, k, v, status)
     T, H, D = _slot_list(slots), cache.heads, cache.head_dim
     if k is None:
-        k = torch.empty((T, H, D), dtype=out_dtype, device=cache.device)
+        k = slots.new_empty((T, H, D), dtype=out_dtype)
     if v is None:
-        v = torch.empty((T, H, D), dtype=k.dtype, device=cache.device)
+        v = torch.empty_like(k) if k.is_contiguous() else slots.new_empty((T, H, D), dtype=k.dtype)
     if k.dtype != v.dtype:
         raise TypeError("k and v share one dtype")
     ks, vs = _token_rows(k, "k", T, H, D), _token_rows(v, "v", T, H, D)
@@ -762,7 +762,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out: contiguous, with q's shape and dtype")
     if lse is None:
-        lse = torch.empty((B, L, HQ), dtype=torch.float32, device=q.device)
+        lse = seq_lens.new_empty((B, L, HQ), dtype=torch.float32)
     elif lse.shape != (B, L, HQ) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse: contiguous float32 [batch, q_tokens, q_heads]")
     ws = kv_attention_workspace(q, cache, page_table) if workspace is None else workspace
@@ -835,7 +835,7 @@ def linear(x: torch.Tensor, w: LinearWeight, out_dtype=None, out=None, workspace
     else:
         raise ValueError("x: contiguous elements required, and contiguous rows beyond two dimensions")
     if out is None:
-        y = torch.empty((*shape[:-1], w.n), dtype=out_dtype or x.dtype, device=w.device)
+        y = x.new_empty((*shape[:-1], w.n), dtype=out_dtype or x.dtype)
     else:
         y = out
         if y.shape != (*shape[:-1], w.n) or not y.is_contiguous() or (out_dtype is not None and y.dtype != out_dtype):
