@@ -47,6 +47,9 @@ inline fp4::KvCache device_cache(const fp4_kv_cache &c)
     d.heads = c.heads;
     d.blocks = c.head_dim / (c.format == FP4_NVFP4 ? 16 : 32);
     d.page = c.page_size;
+    const int64_t granules = d.slots / 16, per = c.page_size / 16;
+    d.narrow = d.slots < ((int64_t)1 << 31) / (c.heads * (c.head_dim / 16)) && granules < ((int64_t)1 << 32) / per;
+    d.magic32 = per > 1 ? ~(uint32_t)0 / (uint32_t)per + 1 : 0;
     return d;
 }
 

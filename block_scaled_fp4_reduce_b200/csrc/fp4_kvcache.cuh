@@ -29,13 +29,30 @@ struct KvCache {
     int64_t slots;       // num_pages * page_size
     uint64_t page_magic; // 2^64 / page, rounded up: slots lie below 2^40
     int heads, blocks, page; // blocks of a token's head: head_dim / G
+    bool narrow;             // a slot's units of 16 elements can be numbered with 31 bits, and
+    uint32_t magic32;        // slot / 16 divided by page / 16 (2^32 over it, rounded up; 0 for 1) in 32
 };
 
-// Row (token of one head) of a slot.
-__device__ __forceinline__ int64_t kv_row(const KvCache &c, int64_t slot, int head)
+// Where a head's block (or 16-code unit) of a slot lies, in units:
+//   (page heads + head) page_size units + (slot - page page_size) units + block
+//   = slot units + page skip + first.
+struct KvPlace {
+    int64_t first, skip;
+};
+
+__device__ __forceinline__ KvPlace kv_place(const KvCache &c, int units, int head, int block)
 {
+    return {(int64_t)head * c.page * units + block, (int64_t)(c.heads - 1) * c.page * units};
+}
+
+__device__ __forceinline__ int64_t kv_at(const KvCache &c, const KvPlace &p, int units, int64_t slot)
+{
+    if (c.narrow) {
+        const uint32_t n = (uint32_t)slot, page = c.magic32 ? __umulhi(n >> 4, c.magic32) : n >> 4;
+        return (int64_t)(n * (uint32_t)units + page * (uint32_t)p.skip + (uint32_t)p.first);
+    }
     const int64_t page = (int64_t)__umul64hi((uint64_t)slot, c.page_magic);
-    return (page * c.heads + head) * c.page + (slot - page * c.page);
+    return slot * units + page * p.skip + p.first;
 }
 
 // The share of one thread: a unit is one block of one head of the keys or
@@ -100,6 +117,7 @@ __global__ void __launch_bounds__(kThreads, kNv && sizeof(T) == 2 ? 4 : 1)
     }
     const T *x = (u.sel ? v : k) + (int64_t)(u.head * c.blocks + u.block) * G;
     const int64_t stride = u.sel ? v_stride : k_stride;
+    const KvPlace place = kv_place(c, c.blocks, u.head, u.block);
     // (not indexed by u.sel: that would copy the arguments to local memory)
     uint8_t *const packed = u.sel ? c.packed[1] : c.packed[0], *const scales = u.sel ? c.scales[1] : c.scales[0];
     int32_t err = 0;
@@ -129,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, kNv && sizeof(T) == 2 ? 4 : 1)
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (at[i] >= 0)
-                at[i] = kv_row(c, at[i], u.head) * c.blocks + u.block;
+                at[i] = kv_at(c, place, c.blocks, at[i]);
         if constexpr (kShared) {
             uint2 pk[U];
             uint32_t code[U];
@@ -185,6 +203,7 @@ __global__ void __launch_bounds__(kThreads)
         return;
     const float g = kNv ? __ldcg((u.sel ? c.g[1] : c.g[0]) + u.head) : 1.0f;
     const uint64_t g2 = pack2(g, g);
+    const KvPlace place = kv_place(c, units, u.head, u.block);
     T *y = (u.sel ? v : k) + (int64_t)(u.head * units + u.block) * 16;
     const int64_t stride = u.sel ? v_stride : k_stride;
     const uint2 *const packed = reinterpret_cast<const uint2 *>(u.sel ? c.packed[1] : c.packed[0]);
@@ -205,7 +224,7 @@ __global__ void __launch_bounds__(kThreads)
             if (next[i] >= c.slots) {
                 bad = true;
             } else if (next[i] >= 0) {
-                const int64_t at = kv_row(c, next[i], u.head) * units + u.block;
+                const int64_t at = kv_at(c, place, units, next[i]);
                 pk[i] = __ldcg(packed + at);
                 sbyte[i] = __ldcg(scales + (kNv ? at : at >> 1));
             }

@@ -101,6 +101,13 @@ def test_write_and_read_are_the_oracle_bit_for_bit(T, H, D, page, skip, dtype, f
     c.check()
 
 
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_write_and_read_where_places_are_formed_with_64_bits(dtype, fmt):
+    """Pages of 2^20 tokens: the 32-bit division by the page size does not reach."""
+    test_write_and_read_are_the_oracle_bit_for_bit(1000, 1, 32, 1 << 20, 7, dtype, fmt, 0)
+
+
 def test_read_into_a_strided_view_leaves_its_neighbours():
     g = gen(3)
     c = make_cache(g, 3, 2, 64, 16, NV)
