@@ -34,10 +34,10 @@
 //
 // MXFP4: a block scale 2^e does not fit fp16.  Inside a token the scales are
 // taken relative to the token's largest, 2^(e - E) (0 below 2^-24); 2^E of a
-// key multiplies the finished score in fp32, 2^E of a value joins the softmax
-// weight: the weights' own reference is m' = max_j (x_j + E_j), beside the
-// softmax's m, so that no value, however large or small, pushes another's
-// weight out of fp16's range.
+// key multiplies the finished score in fp32 (attn_factor), 2^E of a value joins
+// the softmax weight: the weights' own reference is m' = max_j (x_j + E_j),
+// beside the softmax's m, so that no value, however large or small, pushes
+// another's weight out of fp16's range.
 //
 // What bounds it: the issue slots.  A step of 32 tokens (D = 128, 8 rows) takes
 // 601 warp instructions, 2.3 per element and lane: 256 E2M1 conversions and
@@ -206,6 +206,21 @@ template <bool kNv> __device__ __forceinline__ AttnScale attn_scale(float gv, fl
         }
     }
     return s;
+}
+
+// The factor of a row's scores, scale 2^e, in two: between them MXFP4 multiplies
+// the token's 2^E, and with halves on both sides of it no product leaves fp32's
+// range that the score itself does not (a sum of 2^24 times E = 118 would,
+// whatever the factor behind it).
+struct AttnFactor {
+    float f, f2;
+};
+
+__device__ __forceinline__ AttnFactor attn_factor(float scale, int e)
+{
+    const double f = (double)scale * __hiloint2double((1023 + e) << 20, 0); // exact
+    const int half = (((__double2hiint(f) >> 20) & 0x7FF) - 1023) >> 1;     // (of zero: 2^-512 below, zero as well)
+    return {(float)(f * __hiloint2double((1023 - half) << 20, 0)), (float)__hiloint2double((1023 + half) << 20, 0)};
 }
 
 __device__ __forceinline__ float attn_lse(float m, float l)
@@ -510,7 +525,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
     constexpr int KS = D / 16; // k steps of the scores = 16-element tiles of the output
     constexpr int R = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_exp[R]; // 2^(exponent taken out of the row)
+    __shared__ AttnFactor s_factor[R];
 
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     pdl_begin();
@@ -712,12 +727,13 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
                 }
             }
             if (lane == 0)
-                s_exp[r] = __uint_as_float((uint32_t)(127 + (ex - 14)) << 23);
+                s_factor[r] = kNv ? AttnFactor{a.scale * gk * __uint_as_float((uint32_t)(127 + (ex - 14)) << 23), 1.0f}
+                                  : attn_factor(a.scale, ex - 14);
         }
         __syncthreads();
         // Q's operand: lane (g, t) holds row g, elements t D/4 + 4 s .. + 3 of k step s
         uint32_t qb[kParts][NT][KS][2];
-        float rowc[NT][2];     // score of rows 2t, 2t + 1 in units of log2
+        AttnFactor rowc[NT][2]; // of the scores of rows 2t, 2t + 1, in units of log2 (NVFP4: one)
         int last[NT][2], first[NT][2]; // their visible positions
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -732,7 +748,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = n * 8 + 2 * t + e;
-                rowc[n][e] = a.scale * gk * s_exp[r];
+                rowc[n][e] = s_factor[r];
                 last[n][e] = r < rows ? sp.n - a.q_tokens + attn_token(a, row0 + r) : -1;
                 first[n][e] = a.window > 0 ? last[n][e] - (int)min(a.window, (int64_t)0x40000000) + 1 : 0;
             }
@@ -886,9 +902,10 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
                         float v = acc[0][n][e];
                         if constexpr (kParts == 2)
                             v = fmaf(acc[1][n][e], 0x1p-11f, v);
+                        v *= rowc[n][e & 1].f;
                         if constexpr (!kNv)
-                            v *= tokf[e >> 1];
-                        x[n][mt][e] = v * rowc[n][e & 1];
+                            v = v * tokf[e >> 1] * rowc[n][e & 1].f2;
+                        x[n][mt][e] = v;
                     }
             }
             if (edge) {

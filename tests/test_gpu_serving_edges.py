@@ -1,0 +1,24 @@
+"""Single-token serving on the GPU at its edges.  References and tolerances as
+in serving_reference.py."""
+import pytest
+import torch
+
+from test_gpu_serving import BF, F32, MX, check_attention, gen, make_cache, randn, tables
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------- attention: the range --
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("key,query,scale", [
+    (105, 0, -111), (118, 0, -123), (118, -60, -64), (110, -110, -5), (118, -112, -8),
+    (-120, 0, 114), (-110, 110, -5), (-120, 120, -5), (-60, -60, 114), (60, 60, -126)])
+def test_attention_mxfp4_keys_of_every_size(key, query, scale, dtype):
+    """Block scales of the keys round 2^key, queries round 2^query: the factors leave fp32's range, the scores do not."""
+    g = gen(key + query)
+    c = make_cache(g, 4, 2, 128, 32, MX)
+    c.k_scales.copy_(torch.randint(123 + key, 128 + key, c.k_scales.shape, generator=g, dtype=torch.uint8))
+    table = tables(g, 1, 4, 4)
+    q = (randn(g, 1, 2, 8, 128, dtype=F32) * 2.0 ** query).to(dtype)
+    check_attention(c, q, table, [111], 2.0 ** scale, 0)
