@@ -208,17 +208,20 @@ template <bool kNv> __device__ __forceinline__ AttnScale attn_scale(float gv, fl
     return s;
 }
 
-// The factor of a row's scores, scale 2^e, in two: between them MXFP4 multiplies
-// the token's 2^E, and with halves on both sides of it no product leaves fp32's
-// range that the score itself does not (a sum of 2^24 times E = 118 would,
-// whatever the factor behind it).
+// The factor of a row's scores, scale g 2^e (g 1 for MXFP4).  In 64 bits: scale g
+// alone may leave fp32's normal numbers.  MXFP4 multiplies the token's 2^E as well,
+// and with halves of the factor on both sides of it no product leaves fp32's range
+// that the score itself does not (a sum of 2^24 times E = 118 would, whatever the
+// factor behind it).
 struct AttnFactor {
     float f, f2;
 };
 
-__device__ __forceinline__ AttnFactor attn_factor(float scale, int e)
+template <bool kNv> __device__ __forceinline__ AttnFactor attn_factor(float scale, float g, int e)
 {
-    const double f = (double)scale * __hiloint2double((1023 + e) << 20, 0); // exact
+    const double f = (double)scale * g * __hiloint2double((1023 + e) << 20, 0); // exact
+    if constexpr (kNv)
+        return {(float)f, 1.0f};
     const int half = (((__double2hiint(f) >> 20) & 0x7FF) - 1023) >> 1;     // (of zero: 2^-512 below, zero as well)
     return {(float)(f * __hiloint2double((1023 - half) << 20, 0)), (float)__hiloint2double((1023 + half) << 20, 0)};
 }
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
     constexpr int KS = D / 16; // k steps of the scores = 16-element tiles of the output
     constexpr int R = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ AttnFactor s_factor[R];
+    __shared__ int s_exp[R]; // exponent of the power of two taken out of the row
 
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     pdl_begin();
@@ -727,8 +730,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
                 }
             }
             if (lane == 0)
-                s_factor[r] = kNv ? AttnFactor{a.scale * gk * __uint_as_float((uint32_t)(127 + (ex - 14)) << 23), 1.0f}
-                                  : attn_factor(a.scale, ex - 14);
+                s_exp[r] = ex - 14;
         }
         __syncthreads();
         // Q's operand: lane (g, t) holds row g, elements t D/4 + 4 s .. + 3 of k step s
@@ -748,7 +750,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = n * 8 + 2 * t + e;
-                rowc[n][e] = s_factor[r];
+                rowc[n][e] = attn_factor<kNv>(a.scale, gk, s_exp[r]);
                 last[n][e] = r < rows ? sp.n - a.q_tokens + attn_token(a, row0 + r) : -1;
                 first[n][e] = a.window > 0 ? last[n][e] - (int)min(a.window, (int64_t)0x40000000) + 1 : 0;
             }

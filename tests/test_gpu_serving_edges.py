@@ -3,7 +3,7 @@ in serving_reference.py."""
 import pytest
 import torch
 
-from test_gpu_serving import BF, F32, MX, check_attention, gen, make_cache, randn, tables
+from test_gpu_serving import BF, F32, MX, NV, check_attention, gen, make_cache, randn, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -21,4 +21,18 @@ def test_attention_mxfp4_keys_of_every_size(key, query, scale, dtype):
     c.k_scales.copy_(torch.randint(123 + key, 128 + key, c.k_scales.shape, generator=g, dtype=torch.uint8))
     table = tables(g, 1, 4, 4)
     q = (randn(g, 1, 2, 8, 128, dtype=F32) * 2.0 ** query).to(dtype)
+    check_attention(c, q, table, [111], 2.0 ** scale, 0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("key,query,scale,lo,hi", [(-126, 126, -13, 96, 127), (-126, 125, -12, 96, 127), (110, -120, 19, 1, 8), (115, -123, 14, 1, 8),
+                                                   (-60, -60, 113, 40, 64)])
+def test_attention_nvfp4_global_scales_of_every_size(key, query, scale, lo, hi, dtype):
+    """Global scales of the keys round 2^key: times softmax_scale they leave fp32's normal numbers, the scores do not."""
+    g = gen(key + query + 1000)
+    c = make_cache(g, 4, 2, 64, 32, NV)
+    c.k_global_scale.copy_(torch.tensor([1.0, 1.25]) * 2.0 ** key)
+    c.k_scales.copy_(torch.randint(lo, hi, c.k_scales.shape, generator=g, dtype=torch.uint8))
+    table = tables(g, 1, 4, 4)
+    q = (randn(g, 1, 2, 8, 64, dtype=F32).clamp(-3, 3) * 2.0 ** query).to(dtype)
     check_attention(c, q, table, [111], 2.0 ** scale, 0)
