@@ -186,8 +186,9 @@ __device__ __forceinline__ int attn_token(const AttnArgs &a, int r)
     return a.q_tokens == 1 ? 0 : a.group == 1 ? r : (int)__umul64hi((uint64_t)(uint32_t)r, a.group_magic);
 }
 
-// What turns a row's summed output into its result: g / l, and for MXFP4
-// 2^(m' - m), in two factors because the power alone may leave fp32's range.
+// What turns a row's summed output into its result: g / l, or for MXFP4
+// 2^(m' - m) / l.  In two factors: the power alone may leave fp32's range, and
+// g / l its normal numbers where g itself does not.
 // (Sums and weights both carry 2^kAttnBias.)
 struct AttnScale {
     float f, f2;
@@ -198,7 +199,8 @@ template <bool kNv> __device__ __forceinline__ AttnScale attn_scale(float gv, fl
     AttnScale s = {0.0f, 1.0f};
     if (l > 0.0f) {
         if constexpr (kNv) {
-            s.f = gv / l;
+            s.f = 1.0f / l;
+            s.f2 = gv;
         } else {
             const float half = rintf(0.5f * (mw - m));
             s.f = ex2(half) / l;

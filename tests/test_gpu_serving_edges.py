@@ -1,9 +1,12 @@
 """Single-token serving on the GPU at its edges.  References and tolerances as
 in serving_reference.py."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_serving import BF, F32, MX, NV, check_attention, gen, make_cache, randn, tables
+import block_scaled_fp4_reduce_b200 as fp4
+import serving_reference as ref
+from test_gpu_serving import BF, F32, MX, NV, check_attention, gen, make_cache, randn, sequences, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +39,24 @@ def test_attention_nvfp4_global_scales_of_every_size(key, query, scale, lo, hi, 
     table = tables(g, 1, 4, 4)
     q = (randn(g, 1, 2, 8, 64, dtype=F32).clamp(-3, 3) * 2.0 ** query).to(dtype)
     check_attention(c, q, table, [111], 2.0 ** scale, 0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("n", [111, 3000])
+@pytest.mark.parametrize("fmt,size", [(NV, -126), (NV, -110), (NV, 108), (MX, -116), (MX, 118)])
+def test_attention_values_of_every_size(fmt, size, n, dtype):
+    """Values round 2^size, compared relative to it (no absolute allowance but the spacing of numbers below the smallest normal one)."""
+    g = gen(size + n)
+    c = make_cache(g, 50, 2, 64, 64, fmt)
+    if fmt == NV:
+        c.v_global_scale.copy_(torch.tensor([1.0, 1.25]) * 2.0 ** size)
+    else:
+        c.v_scales.copy_(torch.randint(124 + size, 128 + size, c.v_scales.shape, generator=g, dtype=torch.uint8))
+    table = tables(g, 1, 47, 50)
+    q = randn(g, 1, 1, 8, 64, dtype=dtype)
+    out, lse = fp4.kv_attention(q, c, table, torch.tensor([n], dtype=torch.int32).cuda(), scale=0.003)
+    c.check()
+    want, _, tol, _ = ref.attention(q, *sequences(c, table, [n]), [n], 0.003, 0, fmt == MX)
+    tol = tol + ref.HALF[dtype] * np.abs(want) + {BF: 2.0 ** -134, F32: 2.0 ** -150}[dtype]
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= tol).all(), np.max(err / tol)
