@@ -230,7 +230,7 @@ template <bool kNv> __device__ __forceinline__ AttnFactor attn_factor(float scal
 
 __device__ __forceinline__ float attn_lse(float m, float l)
 {
-    return l > 0.0f ? (m + (log2f(l) - kAttnBias)) * kLn2 : -INFINITY;
+    return l == 0.0f ? -INFINITY : (m + (log2f(l) - kAttnBias)) * kLn2; // (NaN of a NaN)
 }
 
 // Place of a row's result among the rows of out and lse.
@@ -913,15 +913,36 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtas<TQ, D, NT>) kv_attenti
                     }
             }
             if (edge) {
+                // A NaN among a token's value scales would reach the rows that do not
+                // see the token as well, 0 times NaN: it is taken out of the values
+                // and put into the scores of the rows that do.  (MXFP4: 2^E of a value
+                // joins the weight, so a weight of 0 stays one.)
+                uint32_t nan = 0;
+                if (kNv && a.q_tokens > 1) { // (rows of one new token see the same)
+                    bool mine = false;
+#pragma unroll
+                    for (int i = 0; i < NB; i += 4) // a byte with seven bits set
+                        mine |= __vcmpeq4(*reinterpret_cast<const uint32_t *>(vs + lane * NB + i) & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
+                    nan = __ballot_sync(0xFFFFFFFFu, mine);
+                    if (nan) {
+                        if (mine)
+#pragma unroll
+                            for (int i = 0; i < NB; i += 4)
+                                *reinterpret_cast<uint32_t *>(vs + lane * NB + i) = 0u;
+                        __syncwarp();
+                    }
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int j = tok + mt * 16 + (e >> 1) * 8 + g;
+                            const int k = mt * 16 + (e >> 1) * 8 + g, j = tok + k;
                             if (j > last[n][e & 1] || j < first[n][e & 1])
                                 x[n][mt][e] = -INFINITY;
+                            else if (nan >> k & 1u)
+                                x[n][mt][e] = NAN;
                         }
             }
 

@@ -532,7 +532,9 @@ fp4_status fp4_kv_read(const fp4_kv_cache *cache, const int64_t *slots, int64_t 
  * A length below 0 or above table_width * page_size sets INDEX, as does a
  * page outside the cache that a visible position names; that sequence's
  * outputs are then unspecified, the others' are not.  A NaN or Inf in a
- * query sets NONFINITE, with that token's outputs unspecified.  Scores,
+ * query sets NONFINITE, with that token's outputs unspecified.  A NaN scale
+ * byte at a position leaves the outputs of the tokens that see it unspecified,
+ * and no others.  Scores,
  * softmax statistics and sums are fp32, q and the softmax weights enter the
  * tensor cores as fp16 (two terms of it for fp32 q).  MXFP4: inside one token
  * and head, what a block holds below 2^-24 of the head's largest block scale

@@ -60,3 +60,41 @@ def test_attention_values_of_every_size(fmt, size, n, dtype):
     tol = tol + ref.HALF[dtype] * np.abs(want) + {BF: 2.0 ** -134, F32: 2.0 ** -150}[dtype]
     err = np.abs(out.double().cpu().numpy() - want)
     assert (err <= tol).all(), np.max(err / tol)
+
+
+# ------------------------------------------------ attention: NaN out of sight --
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+@pytest.mark.parametrize("n,new,window,group,dim,bad", [
+    (100, 4, 0, 2, 64, 99), (100, 4, 0, 2, 128, 97), (100, 4, 40, 2, 64, 57), (33, 3, 0, 1, 256, 32), (1300, 2, 900, 3, 64, 399),
+    (2600, 4, 0, 4, 128, 2598)])
+def test_a_token_s_nan_reaches_the_tokens_that_see_it_and_no_others(n, new, window, group, dim, bad, fmt, dtype):
+    """NaN scale bytes of the key, of the value or of both at a position that some of the new tokens see and others do not."""
+    g = gen(n + bad)
+    c = make_cache(g, 45, 2, dim, 64, fmt)
+    table = torch.randperm(45, generator=g)[:-(-n // 64)][None].int().cuda()
+    if n > 1024:  # a table wide enough for the tokens to be shared out
+        table = torch.cat((table, torch.full((1, 4), -1, dtype=torch.int32, device="cuda")), 1)
+    q = randn(g, 1, new, 2 * group, dim, dtype=dtype)
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    want = fp4.kv_attention(q, c, table, lens, scale=0.01, window=window)
+    pos = n - new + np.arange(new)
+    sees = (bad <= pos) & ((bad > pos - window) if window else True)
+    assert sees.any() and not sees.all()
+    page, off = int(table[0, bad // 64]), bad % 64
+    for names in (("k",), ("v",), ("k", "v")):
+        kept = {name: getattr(c, name + "_scales")[page, 1, off].clone() for name in names}
+        for name in names:
+            getattr(c, name + "_scales")[page, 1, off, -1] = 0x7F if fmt == NV else 0xFF
+        out, lse = fp4.kv_attention(q, c, table, lens, scale=0.01, window=window)
+        c.check()
+        for name in names:
+            getattr(c, name + "_scales")[page, 1, off] = kept[name]
+        for i in range(new):
+            if sees[i]:
+                assert torch.equal(out[0, i, :group], want[0][0, i, :group])  # the other KV head's
+                if fmt == NV or "k" in names:
+                    assert out[0, i, group:].isnan().any(-1).all() and lse[0, i, group:].isnan().all()
+            else:
+                assert torch.equal(out[0, i], want[0][0, i]) and torch.equal(lse[0, i], want[1][0, i])
