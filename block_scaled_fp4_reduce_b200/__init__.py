@@ -808,7 +808,14 @@ class LinearWeight:
 def linear_weight(q: Quantized, stream=None) -> LinearWeight:
     """The quantised weight [n, k] (nvfp4_quantize, mxfp4_quantize, the
     padded and column-wise layouts, ...) laid out for `linear`, once."""
-    return LinearWeight(q.fmt, q.packed, scales_to_mma(q.scales, stream), q.global_scale, q.rows, q.cols)
+    index = q.packed.get_device()
+    if stream is not None:
+        with _on(stream, index):
+            return linear_weight(q)
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return linear_weight(q)
+    return LinearWeight(q.fmt, q.packed, scales_to_mma(q.scales), q.global_scale, q.rows, q.cols)
 
 
 def linear_workspace(rows: int, w: LinearWeight) -> torch.Tensor:

@@ -98,3 +98,26 @@ def test_a_token_s_nan_reaches_the_tokens_that_see_it_and_no_others(n, new, wind
                     assert out[0, i, group:].isnan().any(-1).all() and lse[0, i, group:].isnan().all()
             else:
                 assert torch.equal(out[0, i], want[0][0, i]) and torch.equal(lse[0, i], want[1][0, i])
+
+
+# --------------------------------------------------------- linear: the handle --
+
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_a_weight_laid_out_on_a_given_stream_belongs_to_it(handle):
+    """The current stream held up: layout and status word are ordered with the given stream's calls."""
+    g = gen(77)
+    q = fp4.nvfp4_quantize(randn(g, 300, 2048, scale=0.02))
+    x = randn(g, 20, 2048)
+    want = fp4.linear(x, fp4.linear_weight(q))
+    bad = x.clone()
+    bad[3, 5] = float("inf")
+    side = torch.cuda.Stream()
+    given = side.cuda_stream if handle else side
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    w = fp4.linear_weight(q, stream=given)
+    got = fp4.linear(x, w, stream=given)
+    fp4.linear(bad, w, stream=given)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert int(w.status.item()) == fp4.ERR_NONFINITE  # not wiped out by a zero-fill that came late
