@@ -808,7 +808,8 @@ class LinearWeight:
 def linear_weight(q: Quantized, stream=None) -> LinearWeight:
     """The quantised weight [n, k] (nvfp4_quantize, mxfp4_quantize, the
     padded and column-wise layouts, ...) laid out for `linear`, once."""
-    index = q.packed.get_device()
+    index = _cuda(q.packed, "packed").get_device()
+    _same_device(index, q.scales)
     if stream is not None:
         with _on(stream, index):
             return linear_weight(q)

@@ -132,3 +132,11 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         fp4.KVCache(fp4.NVFP4, t, t, t, t)
     with pytest.raises(ValueError, match="CUDA"):
         fp4.LinearWeight(fp4.NVFP4, torch.zeros(4, 16, dtype=torch.uint8), t, torch.ones(1), 4, 32)
+
+
+def test_linear_weight_refuses_cpu_tensors():
+    """Before the layout kernel is launched on host addresses."""
+    t = torch.zeros(4, 16, dtype=torch.uint8)
+    q = fp4.Quantized(fp4.NVFP4, t, torch.zeros(4, 2, dtype=torch.uint8), torch.ones(1), torch.zeros(1, dtype=torch.int32), 4, 32)
+    with pytest.raises(ValueError, match="CUDA"):
+        fp4.linear_weight(q)
