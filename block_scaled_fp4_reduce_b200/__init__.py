@@ -777,13 +777,17 @@ def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_
 class LinearWeight:
     """An FP4 weight [n, k] laid out for `linear`: packed codes [n, Kp/2]
     (padded layout), the scale bytes in the MMA layout, the NVFP4 global
-    scale (None for MXFP4).  `status` as for KVCache."""
+    scale (None for MXFP4).  Kp, k rounded up to whole blocks, is a multiple
+    of 32: an NVFP4 weight of an odd number of blocks a row is refused.
+    `status` as for KVCache."""
 
     def __init__(self, fmt, packed, scales_mma, global_scale, n: int, k: int, status=None):
         group = 16 if fmt == NVFP4 else 32
         kp = _padded(k, group)
         if fmt not in (NVFP4, MXFP4):
             raise ValueError("fmt: NVFP4 or MXFP4")
+        if kp % 32:
+            raise ValueError(f"k: rounded up to whole blocks of {group} a multiple of 32 required, got {k}")
         dev, self.index = _cuda(packed, "packed", torch.uint8).device, packed.get_device()
         _cuda(scales_mma, "scales_mma", torch.uint8)
         if packed.numel() != n * kp // 2 or not packed.is_contiguous():

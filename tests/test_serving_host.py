@@ -140,3 +140,13 @@ def test_linear_weight_refuses_cpu_tensors():
     q = fp4.Quantized(fp4.NVFP4, t, torch.zeros(4, 2, dtype=torch.uint8), torch.ones(1), torch.zeros(1, dtype=torch.int32), 4, 32)
     with pytest.raises(ValueError, match="CUDA"):
         fp4.linear_weight(q)
+
+
+@pytest.mark.parametrize("k,fits", [(16, False), (48, False), (240, False), (225, False), (224, True), (255, True), (32, True)])
+def test_linear_weight_names_the_k_it_takes(k, fits):
+    """An NVFP4 weight of an odd number of 16-blocks is refused when it is laid out, not by every call with it."""
+    t = torch.zeros(4, 16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA" if fits else "multiple of 32"):
+        fp4.LinearWeight(fp4.NVFP4, t, t, torch.ones(1), 4, k)
+    with pytest.raises(ValueError, match="CUDA"):
+        fp4.LinearWeight(fp4.MXFP4, t, t, None, 4, k)
