@@ -6,7 +6,8 @@ import torch
 
 import block_scaled_fp4_reduce_b200 as fp4
 import serving_reference as ref
-from test_gpu_serving import BF, F32, MX, NV, check_attention, gen, make_cache, randn, sequences, tables
+from test_gpu_serving import (BF, F32, MX, NV, check_attention, gen, host, make_cache, randn, sequences, tables,
+                              test_write_and_read_are_the_oracle_bit_for_bit as oracle_bits)
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +122,101 @@ def test_a_weight_laid_out_on_a_given_stream_belongs_to_it(handle):
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     assert int(w.status.item()) == fp4.ERR_NONFINITE  # not wiped out by a zero-fill that came late
+
+
+# ------------------------------------------- the cache: rounds of its token loop --
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fmt,T,H,D,page,skip", [
+    # two tokens a CTA: 592 CTAs write 2368 a round, 740 read 2960, the last round ending in the first token of a thread and in the second
+    (NV, 8195, 8, 128, 64, 3), (NV, 8900, 8, 128, 48, 0),
+    # 512 units a row: two CTAs side by side; 256 (MXFP4): one token a CTA
+    (NV, 5003, 16, 256, 64, 3), (MX, 5003, 16, 256, 64, 3)])
+def test_write_and_read_of_many_rounds_a_thread(fmt, T, H, D, page, skip, dtype):
+    oracle_bits(T, H, D, page, skip, dtype, fmt, 0)
+
+
+# ------------------------------------------- attention: long shares of a CTA --
+
+NEEDLES = 30
+
+
+def needle_cache(g, heads, dim, page, fmt, background=40):
+    """`background` pages of noise and NEEDLES pages more with one token each (in their first, last or a middle slot) that
+    scores far above it for a query along base [heads, dim]."""
+    c = fp4.kv_cache(background + NEEDLES, heads, dim, page, fmt)
+    slots = torch.arange(c.num_pages * page)
+    k, v = randn(g, len(slots), heads, dim), randn(g, len(slots), heads, dim)
+    base = (torch.randint(0, 2, (heads, dim), generator=g) * 2 - 1).to(BF).cuda()
+    for i in range(NEEDLES):
+        k[(background + i) * page + (0, page - 1, (7 * i) % page)[i % 3]] = base * 2.25
+    fp4.kv_write(c, k, v, slots.cuda())
+    c.check()
+    return c, base
+
+
+def needle_table(g, lens, width, page, background=40):
+    """Noise pages in any order, and every needle page once a sequence: round multiples of 2048 tokens, at the ends, and anywhere."""
+    table = torch.randint(0, background, (len(lens), width), generator=g, dtype=torch.int32)
+    for b, n in enumerate(lens):
+        whole = n // page
+        if whole < NEEDLES:
+            continue
+        at = {0, whole - 1} | {m * 2048 // page + d for m in range(1, n // 2048, max(1, n // 2048 // 6)) for d in (-1, 0)}
+        at = sorted(at)[:NEEDLES - 8]
+        rest = [p for p in torch.randperm(whole, generator=g).tolist() if p not in at][:NEEDLES - len(at)]
+        for i, p in enumerate(at + rest):
+            table[b, p] = background + i
+        table[b, -(-n // page):] = -1
+    return table.cuda()
+
+
+LONG = [  # lens, new, heads, group, dim, page, window: more than 16 rounds of 128 tokens for each of 740, 592 or 444 CTAs
+    ([60001, 20480, 49999, 33333, 55000], 1, 8, 1, 64, 64, 0),
+    ([60000, 41000, 33, 63333], 1, 8, 1, 128, 48, 0),
+    ([60000, 41000, 33333, 47000], 4, 8, 3, 64, 64, 40001),
+]
+
+
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+@pytest.mark.parametrize("lens,new,heads,group,dim,page,window", LONG)
+def test_attention_of_long_shares(lens, new, heads, group, dim, page, window, fmt):
+    g = gen(sum(lens))
+    c, base = needle_cache(g, heads, dim, page, fmt)
+    table = needle_table(g, lens, -(-max(lens) // page) + 1, page)
+    q = base[:, None].expand(heads, group, dim) * (1 + 0.05 * torch.rand(len(lens), new, heads, group, 1, generator=g).cuda())
+    q = q.flatten(2, 3).to(BF)
+    # a needle's score is 7.2 (ln 1340) over a background of e^s, s of deviation 0.4: 1 to 4 % of a sum
+    check_attention(c, q, table, lens, 7.2 / 2.25 / dim, window)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+@pytest.mark.parametrize("lens,new,heads,group,dim,page,window", LONG + [([5200, 4097, 2049, 1300] + [i % 40 for i in range(750)], 1, 8, 1, 64, 64, 0)])
+def test_attention_counts_every_token_once(lens, new, heads, group, dim, page, window, fmt, dtype):
+    """Queries of zero: every weight is exactly one, and lse the logarithm of the number of visible tokens.  A single token
+    of 63333 lost or taken twice moves it by 1.6e-5; log2f and the product with ln 2 by 2^-22 of it, 3e-6."""
+    g = gen(sum(lens) + 1)
+    c = make_cache(g, 50, heads, dim, page, fmt)
+    table = torch.randint(0, 50, (len(lens), -(-max(lens) // page) + 1), generator=g, dtype=torch.int32).cuda()
+    q = torch.zeros(len(lens), new, heads * group, dim, dtype=dtype, device="cuda")
+    _, lse = fp4.kv_attention(q, c, table, torch.tensor(lens, dtype=torch.int32).cuda(), window=window)
+    c.check()
+    pos = np.array(lens)[:, None] - new + np.arange(new)
+    count = np.maximum(0, np.minimum(pos + 1, window) if window else pos + 1)
+    with np.errstate(divide="ignore"):
+        want = np.log(count)[:, :, None].repeat(heads * group, 2)
+    got = lse.double().cpu().numpy()
+    assert np.array_equal(np.isneginf(got), np.isneginf(want))
+    seen = ~np.isneginf(want)
+    assert (np.abs(got[seen] - want[seen]) <= 2.0 ** -22 * np.abs(want[seen]) + 2.0 ** -20).all()
+
+
+def test_attention_of_a_long_sequence_that_one_cta_takes():
+    """8 units a CTA slot and more under a table of 6400 tokens: a unit is a CTA's, however long it is."""
+    g = gen(79)
+    lens = [5200, 4097, 2049] + [int(i) for i in torch.randint(0, 40, (760,), generator=g)]
+    c, base = needle_cache(g, 8, 64, 64, NV)
+    table = needle_table(g, lens, 100, 64)
+    q = base[None, None].expand(len(lens), 1, 8, 64).contiguous()
+    check_attention(c, q, table, lens, 7.2 / 2.25 / 64, 0)
