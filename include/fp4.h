@@ -580,11 +580,13 @@ fp4_status fp4_linear(fp4_format fmt, const void *x, fp4_dtype dtype, int64_t ro
                       cudaStream_t stream);
 
 /* Tests only: the largest number of work units one launch takes (default
- * 2^30, restored by units = 0; else a multiple of 64 from 64 up).  Every
- * call above splits larger problems into several launches at this limit;
- * lowering it makes small tensors cross those split points.  Process-wide,
- * not thread-safe; set it only while no other call is being made.
- * FP4_ERR_INVALID_ARG for other values. */
+ * 2^30, restored by units = 0; else a multiple of 64 from 64 up).  The
+ * quantisers, the search and the dequantisers of rows, padded rows and groups
+ * split larger problems into several launches at this limit (the other calls
+ * have none of their own: the GEMM, the layouts of its scales, the columns,
+ * the single-token serving calls); lowering it makes small tensors cross
+ * those split points.  Process-wide, not thread-safe; set it only while no
+ * other call is being made.  FP4_ERR_INVALID_ARG for other values. */
 fp4_status fp4_set_launch_unit_limit(int64_t units);
 
 /* Launch planner of the grouped calls alone, for tests (host only, no GPU

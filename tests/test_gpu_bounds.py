@@ -307,3 +307,86 @@ def test_gemm_output(kernel):
         d.check("gemm D")
         assert st.item() == fp4.OK
         assert torch.equal(d.t, ref)
+
+
+@pytest.mark.parametrize("fmt", [fp4.NVFP4, fp4.MXFP4])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,heads,dim,page", [(1, 1, 32, 16), (7, 3, 96, 16), (131, 2, 64, 48), (40, 5, 256, 32)])
+def test_cache_write_and_read(tokens, heads, dim, page, dtype, fmt):
+    pages, nb = -(-tokens // page) + 1, dim // (16 if fmt == fp4.NVFP4 else 32)
+    k, v = (rand(tokens, heads * dim, dtype, seed).view(tokens, heads, dim) for seed in (1, 2))
+    slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(3))[:tokens]
+    slots[0] = pages * page - 1  # the cache's last slot
+    slots[1:][slots[1:] == slots[0]] = -1
+    slots = slots.to(DEV)
+    g = [torch.full((heads,), 1 / 64, device=DEV)] * 2 if fmt == fp4.NVFP4 else [None, None]
+    plain = fp4.kv_cache(pages, heads, dim, page, fmt, 1 / 64, 1 / 64)
+    fp4.kv_write(plain, k, v, slots)
+    kr, vr = fp4.kv_read(plain, slots, dtype)
+    for fill in FILLS:
+        parts = [Guarded((pages, heads, page, n), torch.uint8, fill) for n in (dim // 2, nb, dim // 2, nb)]
+        for part in parts:
+            part.t.zero_()
+        st = Guarded((1,), torch.int32, fill)
+        st.t.zero_()
+        c = fp4.KVCache(fmt, *(part.t for part in parts), *g, status=st.t)
+        fp4.kv_write(c, k, v, slots)
+        ko, vo = Guarded((tokens, heads, dim), dtype, fill), Guarded((tokens, heads, dim), dtype, fill)
+        fp4.kv_read(c, slots, k=ko.t, v=vo.t)
+        torch.cuda.synchronize()
+        for b, what in zip([*parts, st, ko, vo], ("k packed", "k scales", "v packed", "v scales", "status", "k read", "v read")):
+            b.check(what)
+        assert st.t.item() == fp4.OK
+        assert torch.equal(ko.t, kr) and torch.equal(vo.t, vr)
+        for b, name in zip(parts, ("k_packed", "k_scales", "v_packed", "v_scales")):
+            assert torch.equal(b.t, getattr(plain, name))
+
+
+@pytest.mark.parametrize("fmt", [fp4.NVFP4, fp4.MXFP4])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lens,width,new,heads,group,dim", [
+    ([1], 1, 1, 1, 1, 64), ([90, 0, 33], 2, 1, 2, 3, 128), ([100], 2, 5, 1, 5, 256),  # a CTA for each unit
+    ([3000, 17, 0, 4000], 63, 1, 2, 5, 64), ([4000], 80, 3, 1, 4, 128), ([2000, 3999], 64, 1, 1, 8, 256)])  # tokens shared out
+def test_cache_attention(lens, width, new, heads, group, dim, dtype, fmt):
+    B, HQ = len(lens), heads * group
+    c = fp4.kv_cache(70, heads, dim, 64, fmt)
+    n = 70 * 64
+    fp4.kv_write(c, *(rand(n, heads * dim, dtype, seed).view(n, heads, dim) * 20 for seed in (1, 2)), torch.arange(n, device=DEV))
+    table = torch.randint(0, 70, (B, width), generator=torch.Generator().manual_seed(4), dtype=torch.int32).to(DEV)
+    q = rand(B * new, HQ * dim, dtype, 5).view(B, new, HQ, dim)
+    lens = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    want = fp4.kv_attention(q, c, table, lens)
+    for fill in FILLS:
+        out, lse = Guarded(q.shape, dtype, fill), Guarded((B, new, HQ), torch.float32, fill)
+        ws = Guarded((fp4.lib().fp4_kv_attention_workspace_bytes(c._ref, B, new, HQ, width),), torch.uint8, fill)
+        ws.t.zero_()
+        st = Guarded((1,), torch.int32, fill)
+        st.t.zero_()
+        fp4.kv_attention(q, c, table, lens, out=out.t, lse=lse.t, workspace=ws.t, status=st.t)
+        torch.cuda.synchronize()
+        for b, what in ((out, "out"), (lse, "lse"), (ws, "workspace"), (st, "status")):
+            b.check(what)
+        assert st.t.item() == fp4.OK
+        assert torch.equal(out.t, want[0]) and torch.equal(lse.t, want[1])
+
+
+@pytest.mark.parametrize("fmt", [fp4.NVFP4, fp4.MXFP4])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("out_dtype", DTYPES)
+@pytest.mark.parametrize("rows,n,k", [(1, 1, 32), (2, 129, 544), (5, 77, 255), (17, 300, 2080), (33, 130, 96), (201, 70, 160)])
+def test_linear(rows, n, k, dtype, out_dtype, fmt):
+    w = rand(n, k, torch.bfloat16, 6)
+    w = fp4.linear_weight(fp4.nvfp4_quantize_padded(w) if fmt == fp4.NVFP4 else fp4.mxfp4_quantize_padded(w))
+    x = rand(rows, k, dtype, 7)
+    want = fp4.linear(x, w, out_dtype)
+    for fill in FILLS:
+        y = Guarded((rows, n), out_dtype, fill, offset=out_dtype.itemsize)  # aligned to its elements alone
+        ws = Guarded((fp4.lib().fp4_linear_workspace_bytes(rows, k),), torch.uint8, fill)
+        st = Guarded((1,), torch.int32, fill)
+        st.t.zero_()
+        fp4.linear(x, w, out=y.t, workspace=ws.t, status=st.t)
+        torch.cuda.synchronize()
+        for b, what in ((y, "y"), (ws, "workspace"), (st, "status")):
+            b.check(what)
+        assert st.t.item() == fp4.OK
+        assert torch.equal(y.t, want)
