@@ -599,6 +599,22 @@ def _same_device(index: int, *tensors) -> None:
             raise ValueError(f"all tensors of a call live on one device: cuda:{index} and {t.device}")
 
 
+def _status(given, own: torch.Tensor) -> torch.Tensor:
+    """The status word of a call: the given one, or its handle's."""
+    if given is None:
+        return own
+    if given.dtype != torch.int32 or given.numel() < 1:
+        raise TypeError("status: an int32 word required")
+    return given
+
+
+def _workspace(ws: torch.Tensor) -> int:
+    """Its bytes."""
+    if not ws.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor required")
+    return ws.numel() * ws.element_size()
+
+
 class KVCacheStruct(ctypes.Structure):
     """struct fp4_kv_cache (include/fp4.h)."""
     _fields_ = [("format", ctypes.c_int), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
@@ -638,7 +654,7 @@ class KVCache:
         self.fmt, self.device = fmt, dev
         self.k_packed, self.k_scales, self.v_packed, self.v_scales = k_packed, k_scales, v_packed, v_scales
         self.k_global_scale, self.v_global_scale = k_global_scale, v_global_scale
-        self.status = status if status is not None else new_status(dev)
+        self.status = new_status(dev) if status is None else _status(status, status)
         nv = fmt == NVFP4
         self._struct = KVCacheStruct(fmt, self.heads, self.head_dim, self.page_size, self.num_pages, _p(k_packed),
                                      _p(k_scales), _p(v_packed), _p(v_scales), _p(k_global_scale) if nv else None,
@@ -698,7 +714,7 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     if k.dtype != v.dtype:
         raise TypeError("k and v share one dtype")
     ks, vs = _token_rows(k, "k", T, H, D), _token_rows(v, "v", T, H, D)
-    st = cache.status if status is None else status
+    st = _status(status, cache.status)
     _same_device(cache.index, k, v, slots, status)
     _call("fp4_kv_write", cache.index, stream, cache._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k), T, ks, vs,
           slots.data_ptr(), rule, st.data_ptr())
@@ -718,7 +734,7 @@ def kv_read(cache: KVCache, slots: torch.Tensor, out_dtype=torch.bfloat16, k=Non
     if k.dtype != v.dtype:
         raise TypeError("k and v share one dtype")
     ks, vs = _token_rows(k, "k", T, H, D), _token_rows(v, "v", T, H, D)
-    st = cache.status if status is None else status
+    st = _status(status, cache.status)
     _same_device(cache.index, k, v, slots, status)
     _call("fp4_kv_read", cache.index, stream, cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
           _dtype_code(k), ks, vs, st.data_ptr())
@@ -766,11 +782,12 @@ def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_
     elif lse.shape != (B, L, HQ) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse: contiguous float32 [batch, q_tokens, q_heads]")
     ws = kv_attention_workspace(q, cache, page_table) if workspace is None else workspace
-    st = cache.status if status is None else status
+    ws_bytes = _workspace(ws)
+    st = _status(status, cache.status)
     _same_device(cache.index, q, page_table, seq_lens, out, lse, ws, status)
     _call("fp4_kv_attention", cache.index, stream, cache._ref, q.data_ptr(), _dtype_code(q), B, L, HQ, one,
           page_table.data_ptr(), page_table.size(1), seq_lens.data_ptr(), D ** -0.5 if scale is None else scale, window,
-          out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), st.data_ptr())
+          out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws_bytes, st.data_ptr())
     return out, lse
 
 
@@ -800,7 +817,7 @@ class LinearWeight:
         self.fmt, self.n, self.k, self.device = fmt, n, k, dev
         self.packed, self.scales_mma, self.global_scale = packed, scales_mma, global_scale
         self._packed, self._scales, self._g = _p(packed), _p(scales_mma), _p(global_scale) if fmt == NVFP4 else None
-        self.status = status if status is not None else new_status(dev)
+        self.status = new_status(dev) if status is None else _status(status, status)
 
     def check(self, where: str = "LinearWeight"):
         st = int(self.status.item())
@@ -824,7 +841,8 @@ def linear_weight(q: Quantized, stream=None) -> LinearWeight:
 
 
 def linear_workspace(rows: int, w: LinearWeight) -> torch.Tensor:
-    """A workspace for `linear` calls of up to `rows` rows with w."""
+    """A workspace for `linear` calls of up to `rows` rows with w, on one
+    stream at a time."""
     return torch.empty(max(lib().fp4_linear_workspace_bytes(rows, w.k), 16), dtype=torch.uint8, device=w.device)
 
 
@@ -853,10 +871,11 @@ def linear(x: torch.Tensor, w: LinearWeight, out_dtype=None, out=None, workspace
         if y.shape != (*shape[:-1], w.n) or not y.is_contiguous() or (out_dtype is not None and y.dtype != out_dtype):
             raise ValueError(f"out: contiguous {[*shape[:-1], w.n]} of the output dtype required")
     ws = linear_workspace(rows, w) if workspace is None else workspace
-    st = w.status if status is None else status
+    ws_bytes = _workspace(ws)
+    st = _status(status, w.status)
     _same_device(w.index, x, y, ws, status)
     _call("fp4_linear", w.index, stream, w.fmt, x.data_ptr(), _dtype_code(x), rows, w.k, stride, w._packed,
-          w._scales, w._g, w.n, y.data_ptr(), _dtype_code(y), ws.data_ptr(), ws.numel() * ws.element_size(),
+          w._scales, w._g, w.n, y.data_ptr(), _dtype_code(y), ws.data_ptr(), ws_bytes,
           st.data_ptr())
     return y
 

@@ -220,3 +220,28 @@ def test_attention_of_a_long_sequence_that_one_cta_takes():
     table = needle_table(g, lens, 100, 64)
     q = base[None, None].expand(len(lens), 1, 8, 64).contiguous()
     check_attention(c, q, table, lens, 7.2 / 2.25 / 64, 0)
+
+
+def test_the_helpers_refuse_words_and_workspaces_that_are_not_what_they_seem():
+    """A status that is no int32 word, and a workspace of fewer bytes than elements times their size."""
+    g = gen(80)
+    w = fp4.linear_weight(fp4.nvfp4_quantize(randn(g, 70, 64)))
+    x, slots = randn(g, 3, 64), torch.tensor([1, 2, 3]).cuda()
+    c = make_cache(g, 4, 2, 64, 16, NV)
+    k, table, lens, q = randn(g, 3, 2, 64), tables(g, 1, 4, 4), torch.tensor([60], dtype=torch.int32).cuda(), randn(g, 1, 1, 4, 64)
+    need = fp4.kv_attention_workspace(q, c, table).numel(), fp4.linear_workspace(3, w).numel()
+    one = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    for status in (torch.zeros(1, dtype=torch.uint8, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")):
+        for bad in (lambda: fp4.kv_write(c, k, k, slots, status=status), lambda: fp4.kv_read(c, slots, status=status),
+                    lambda: fp4.kv_attention(q, c, table, lens, status=status), lambda: fp4.linear(x, w, status=status),
+                    lambda: fp4.KVCache(NV, c.k_packed, c.k_scales, c.v_packed, c.v_scales, c.k_global_scale, c.v_global_scale, status),
+                    lambda: fp4.LinearWeight(NV, w.packed, w.scales_mma, w.global_scale, 70, 64, status)):
+            with pytest.raises((TypeError, ValueError), match="status"):
+                bad()
+    for bad in (lambda: fp4.kv_attention(q, c, table, lens, workspace=one[:1].expand(need[0])),
+                lambda: fp4.linear(x, w, workspace=one[:1].expand(need[1]))):
+        with pytest.raises(ValueError, match="workspace"):
+            bad()
+    torch.cuda.synchronize()
+    c.check()
+    w.check()
