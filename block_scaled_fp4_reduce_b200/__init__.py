@@ -755,7 +755,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_
     cache: q [batch, q_tokens, q_heads, head_dim] (bf16 or fp32; a token
     stride is kept), page_table int32 [batch, width], seq_lens int32 [batch]
     (new tokens counted, already written), scale 1/sqrt(head_dim) by default,
-    window 0 = all earlier tokens.  Returns (out, lse [batch, q_tokens,
+    window 0 = all earlier tokens.  head_dim 64, 128 or 256.  Returns (out, lse [batch, q_tokens,
     q_heads] fp32)."""
     if stream is not None and (out is None or lse is None or workspace is None):
         with _on(stream, cache.index):

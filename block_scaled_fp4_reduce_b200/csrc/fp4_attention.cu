@@ -70,14 +70,15 @@ fp4_status launch_attention_t(fp4::AttnArgs a, cudaStream_t stream)
     if (sms <= 0 || !smem_attr(kernel, smem))
         return FP4_ERR_CUDA;
     // A CTA per unit where the table holds few tokens, or the units fill the GPU
-    // several times over; otherwise the tokens are shared out.  Measured (8 heads
-    // x 128, 4 query heads each, us, cold L2, a CTA per unit | shared out): one
-    // sequence of 600 tokens 13.3 | 18.4, 1024 16.4 | 18.4, 1280 18.4 | 18.4,
-    // 2048 22.5 | 18.5; 32 of 1024 20.4 | 26.6, of 4096 47.1 | 47.1.  With many
-    // units a CTA each is faster while the lengths are alike (256 sequences of
-    // 2000 tokens 123 | 133, of 0 to 2000 78 | 84), but a single long sequence
-    // among short ones then takes as long as one CTA needs for it (7 us a
-    // thousand tokens), so that the units have to be many before it is chosen.
+    // several times over; otherwise the tokens are shared out.  Measured (8 heads x
+    // 128, 4 query heads each, cold L2, one call between two events, us, of which these
+    // take about 5, a CTA per unit | shared out): one sequence of 600 tokens 13.3 |
+    // 18.4, 1024 16.4 | 18.4, 1280 18.4 | 18.4, 2048 22.5 | 18.5; 32 of 1024 20.4 |
+    // 26.6, of 4096 47.1 | 47.1.  With many units a CTA each is faster while the
+    // lengths are alike (256 sequences of 2000 tokens 123 | 133, of 0 to 2000 78 | 84),
+    // but a single long sequence among short ones then takes as long as one CTA needs
+    // for it (7 us a thousand tokens), so that the units have to be many before it is
+    // chosen.
     const int64_t units = (int64_t)a.batch * a.c.heads * a.row_tiles, slots = (int64_t)(sms < kMostSms ? sms : kMostSms) * ctas;
     int64_t most = a.capacity;
     if (a.window > 0 && a.window < most - a.q_tokens - 15) // the window, the tile's new tokens, the rounding to 16

@@ -30,7 +30,11 @@
 // rows as two fp16 terms.  Softmax weights enter as fp16 scaled by 2^11 over
 // a reference that the running maximum passes by at most 2^4, so that weights
 // down to 2^-25 of the largest keep all their bits and the rest down to 2^-36
-// some; fp32 calls add a second term.
+// some; fp32 calls add a second term.  For bf16 one is enough: a weight is off by
+// 2^-11 at most, an eighth of the result's own rounding, and the error against
+// 64-bit arithmetic stays the rounding's (0.0016 of the result with one term or
+// fp32 weights); a second term costs 2 x 131071 tokens 71.8 -> 81.5 us, 32 ragged
+// sequences to 8192 43.9 -> 49.9.
 //
 // MXFP4: a block scale 2^e does not fit fp16.  Inside a token the scales are
 // taken relative to the token's largest, 2^(e - E) (0 below 2^-24); 2^E of a
@@ -39,15 +43,17 @@
 // beside the softmax's m, so that no value, however large or small, pushes
 // another's weight out of fp16's range.
 //
-// What bounds it: the issue slots.  A step of 32 tokens (D = 128, 8 rows) takes
-// 601 warp instructions, 2.3 per element and lane: 256 E2M1 conversions and
-// products with the block scale, 64 to interleave nibbles, 32 MMAs, the loads,
-// the softmax; the SMs issue on 61 % of their cycles, with four CTAs of 128
-// registers a thread each.  Measured, cold L2: 2 sequences of 131071 tokens, 8
-// heads x 128, 8 query heads each, 72 us, 302 MB at 4.2 TB/s (0.64 of the copy
-// rate); 32 of 4096 tokens, 4 query heads each, 39 us, 151 MB at 3.9 TB/s.
-// Short calls are latency: the lengths, the page table and the first codes
-// depend on one another (4 us), and joining pieces takes another 3.
+// What bounds it: instructions, and the waits between them.  A step of 32 tokens
+// (D = 128, 8 rows) takes 588 warp instructions, 2.3 per element and lane: 256
+// E2M1 conversions and products with the block scale, 64 to interleave nibbles,
+// 32 MMAs, the loads, the softmax, one dependent chain in each warp; the SMs
+// issue on 60 % of their cycles, with four CTAs of 128 registers a thread each.
+// Measured, GPU time (calls back to back in a graph, three sets of inputs in
+// turn, larger than L2): 2 sequences of 131071 tokens, 8 heads x 128, 8 query
+// heads each, 71 us, 302 MB at 4.2 TB/s (0.65 of the copy rate); 32 of 4096
+// tokens, 4 query heads each, 40 us, 151 MB at 3.8 TB/s.  Short calls are latency:
+// the lengths, the page table and the first codes depend on one another (4 us),
+// and joining pieces takes another 3.
 // Not faster: CTAs of eight warps (2 x 131071 5 % less time, ragged batches 12 %
 // more), and warps of an SM kept in step by barriers.
 #pragma once
@@ -260,12 +266,13 @@ template <typename TQ> __device__ __forceinline__ void attn_write(TQ *dst, float
 // units in that order (heads innermost) and all of this numbered through, CTA i
 // takes the numbers [i s, (i + 1) s), s = the total over the CTAs that fit on
 // the GPU: every CTA has the same work whatever the lengths are, in one wave
-// (short sequences beside long ones: 256 sequences of 0 to 2000 tokens, 8 heads x
-// 128, 4 query heads each, take 131 us where starts count for nothing, 84 so; 3
-// and 4 rounds for a start are no better than 2).  The lengths are on the device, so
-// every CTA forms the numbering for itself, a scan over the sequences.  A CTA
-// whose numbers cross units takes them one after the other; a unit that crosses
-// CTAs leaves pieces, which the CTA that finishes the last of them joins.
+// (short sequences beside long ones: 256 sequences of 0 to 2000 tokens, 8 heads
+// x 128, 4 query heads each, one call between two events: 131 us where starts
+// count for nothing, 84 so; 3 and 4 rounds for a start are no better than 2).
+// The lengths are on the device, so every CTA forms the numbering for itself, a
+// scan over the sequences.  A CTA whose numbers cross units takes them one
+// after the other; a unit that crosses CTAs leaves pieces, which the CTA that
+// finishes the last of them joins.
 // ---------------------------------------------------------------------------
 template <int R> __device__ __forceinline__ uint32_t attn_sequence_rounds(const AttnArgs &a, int len)
 {

@@ -74,10 +74,11 @@ int pick_stages(int cols, int fused, size_t &smem)
 
 // CTAs of a cluster.  A CTA's time is its chunks and about kLinFixed more for
 // its start and end; what counts is that times the rounds the grid takes.  Of
-// one to eight CTAs this picks the fastest or one within 4 % of it (us, cold L2;
-// 1 x 57344 x 14336: 122, 112, 118, 118, 130, 140, 174, 172, picked 3 as 115 to
-// 118; 16 x 8192 x 8192: 33.8, 27.7, 23.6, 21.5, 25.7, .., picked 4; 64 x 4096 x
-// 14336: 66.5, 48.1, 33.8, 29.7, 29.7, 27.7, 25.6, 25.6, picked 8).
+// one to eight CTAs this picks the fastest or one within 4 % of it (cold L2,
+// one call between two events, us; 1 x 57344 x 14336: 122, 112, 118, 118, 130,
+// 140, 174, 172, picked 3 as 115 to 118; 16 x 8192 x 8192: 33.8, 27.7, 23.6,
+// 21.5, 25.7, .., picked 4; 64 x 4096 x 14336: 66.5, 48.1, 33.8, 29.7, 29.7,
+// 27.7, 25.6, 25.6, picked 8).
 int pick_splits(int64_t tiles, int chunks, int64_t slots)
 {
     constexpr int kLinFixed = 6;

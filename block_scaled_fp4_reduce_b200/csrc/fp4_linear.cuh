@@ -32,14 +32,16 @@
 // before the first chunk), 2^(e - E), which is exact down to 2^-23; the row's
 // 2^E multiplies the sum.
 //
-// What bounds it (cold L2): a weight of 57344 x 14336, 462 MB, takes 109 us with
-// one activation row, 157 with 64 (copies alone 82).  The ring keeps HBM busy
+// What bounds it (GPU time, calls back to back in a graph, weights larger than L2
+// together): a weight of 57344 x 14336, 462 MB, takes 109 us with one activation
+// row, 155 with 64 (copies alone 82).  The ring keeps HBM busy
 // while a CTA is in its loop; the starts and ends of its units, about as long as
 // six chunks each, and the last round of the grid are the rest.  With 64 rows the
 // activations that every band of 128 weight rows reads again from L2 are 1.8
-// times the weight's bytes.  A weight of 14336 x 4096 takes 16.6 us with 16 rows,
-// 5 of them its bytes: launch, packing and the first copies 3 us, the sums'
-// way through the cluster 3.
+// times the weight's bytes.  An MXFP4 weight of 14336 x 4096 takes 16.6 us with 16
+// rows: launch, packing and the first copies 3 us, the sums' way through the
+// cluster 3, and 10 for bytes that HBM could bring in 5 (112 bands in two CTAs
+// each leave half the SMs with one CTA where two fit).
 #pragma once
 
 #include <cstdint>
@@ -76,10 +78,10 @@ __host__ __device__ constexpr int lin_landing_bytes(int cols) { return cols <= k
 // Where a CTA's share of the activations is small, the decoders lay it out
 // themselves, in shared memory, while the first codes are on their way: no
 // packing grid and no workspace.  The most rows, and rows x chunks of K.  Laid
-// out by the decoders | packed, us, cold L2, bf16: 1 x 8192 x 4096 (8 chunks a
-// CTA) 14.5 | 16.3, 1 x 14336 x 4096 (16) 18.4 | 18.4, 2 x 8192 x 4096 16.3 |
-// 16.4, 2 x 14336 x 4096 20.4 | 19.5, 4 x 4096 x 4096 (4) 16.4 | 14.3, 8 x 4096
-// x 4096 20.4 | 15.3.
+// out by the decoders | packed, cold L2, one call between two events, us, bf16:
+// 1 x 8192 x 4096 (8 chunks a CTA) 14.5 | 16.3, 1 x 14336 x 4096 (16) 18.4 |
+// 18.4, 2 x 8192 x 4096 16.3 | 16.4, 2 x 14336 x 4096 20.4 | 19.5, 4 x 4096 x
+// 4096 (4) 16.4 | 14.3, 8 x 4096 x 4096 20.4 | 15.3.
 constexpr int kLinFusedRows = 2, kLinFusedShare = 16;
 
 // Codes and scales of a chunk, with its activations where those come packed.
